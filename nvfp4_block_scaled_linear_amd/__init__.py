@@ -29,3 +29,12 @@ from ._binding import (  # noqa: F401
     read_probe,
     status_string,
 )
+from ._mx import (  # noqa: F401
+    MX_EXPORTS,
+    OUT_SWIGLU_MXFP4,
+    mxfp4_dequantize,
+    mxfp4_grouped_linear,
+    mxfp4_grouped_workspace_size,
+    mxfp4_linear,
+    mxfp4_quantize,
+)
