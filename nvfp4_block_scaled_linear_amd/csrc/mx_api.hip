@@ -230,6 +230,8 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
   a.N = N; a.K = K;
   a.tiles = ws.tiles; a.n_tiles = ws.n_tiles; a.offsets = ws.offsets; a.sorted = ws.sorted;
   a.route_expert = ws.route_expert; a.R = R;
+  a.tile_rows = L.tile_rows;
+  a.x_rows = rows_mode == NVFP4_ROWS_PER_TOKEN ? T : R;
   a.rows_per_token = rows_mode == NVFP4_ROWS_PER_TOKEN ? 1 : 0;
   a.top_k = top_k;
   a.y = y; a.y_scales = y_scales; a.ldy = N; a.y_type = y_type;

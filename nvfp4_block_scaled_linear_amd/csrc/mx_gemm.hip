@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64) void mx_tile(MxArgs a) {
   const int64_t N = a.N, K = a.K, half = N >> 1;
   const int64_t cols = SWIGLU ? half : N;
   const int64_t nbn = (cols + kTileCols - 1) / kTileCols;
-  const int64_t tile = blockIdx.x / nbn;
+  const int64_t tile = blockIdx.x / nbn;  // of kTileRows rows; grouped: a part of a list tile
   const int64_t n0 = (blockIdx.x % nbn) * kTileCols;
   const uint8_t* wc = a.w_codes;
   const uint8_t* ws = a.w_scales;
@@ -64,9 +64,13 @@ __global__ __launch_bounds__(64) void mx_tile(MxArgs a) {
   bool row_ok;
   if (GROUPED) {
     if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4 && n0 == 0) clear_dropped_scales(a, tile, kTileRows);
-    if (tile >= *a.n_tiles) return;
-    const int e = a.tiles[2 * tile];
-    const int slot = a.tiles[2 * tile + 1] + c;
+    const int parts = a.tile_rows / kTileRows;
+    const int64_t lt = tile / parts;
+    if (lt >= *a.n_tiles) return;
+    const int e = a.tiles[2 * lt];
+    const int first = a.tiles[2 * lt + 1] + (int)(tile % parts) * kTileRows;
+    if (first >= a.offsets[e + 1]) return;
+    const int slot = first + c;
     row_ok = slot < a.offsets[e + 1];
     yrow = row_ok ? a.sorted[slot] : 0;
     xrow = a.rows_per_token ? yrow / a.top_k : yrow;
@@ -169,11 +173,13 @@ __global__ __launch_bounds__(64) void mx_tile(MxArgs a) {
 
 }  // namespace
 
-int mx_tile_rows(int64_t, int64_t) { return kTileRows; }
+int mx_tile_rows(int64_t R, int64_t active) { return R >= 64 * active ? 128 : kTileRows; }
 
 hipError_t launch_mx_product(const MxArgs& a, int act_kind, int64_t max_tiles, hipStream_t stream) {
+  if ((a.tiles ? a.tile_rows > kTileRows : a.M >= 64) && mx_tiled_takes(a, act_kind))
+    return launch_mx_tiled(a, act_kind, max_tiles, stream);
   const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
-  const int64_t gx = a.tiles ? max_tiles : (a.M + kTileRows - 1) / kTileRows;
+  const int64_t gx = a.tiles ? max_tiles * (a.tile_rows / kTileRows) : (a.M + kTileRows - 1) / kTileRows;
   const int64_t groups = gx * ((cols + kTileCols - 1) / kTileCols);
   if (groups * 64 > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
   const bool bf = act_kind == MXFP4_ACT_BF16;

@@ -27,6 +27,8 @@ struct MxArgs {
   int32_t y_type;
   int32_t swiglu;  // 0, or MXFP4_OUT_SWIGLU_BF16 / MXFP4_OUT_SWIGLU_MXFP4
   // grouped form (NULL tiles for dense): tiles of tile_rows routes of one expert
+  int32_t tile_rows;
+  int64_t x_rows;          // rows of x
   const int32_t* tiles;    // [n_tiles][2] (expert, first slot in sorted)
   const int32_t* n_tiles;  // [1]
   const int32_t* offsets;  // [E+1]
@@ -45,6 +47,9 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 
 // routes of one tile of the grouped form's tile list, for R routes over `active` experts
 int mx_tile_rows(int64_t R, int64_t active);
+// the kernel for LDS tiles (mx_tiled.hip), and whether its 32-bit offsets reach the operands
+bool mx_tiled_takes(const MxArgs& a, int act_kind);
+hipError_t launch_mx_tiled(const MxArgs& a, int act_kind, int64_t max_tiles, hipStream_t stream);
 // max_tiles bounds the tile list of the grouped form (0: dense)
 hipError_t launch_mx_product(const MxArgs& a, int act_kind, int64_t max_tiles, hipStream_t stream);
 

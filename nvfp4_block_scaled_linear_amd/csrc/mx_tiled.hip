@@ -1,0 +1,434 @@
+// MXFP4 products in LDS tiles, for enough activation rows to fill them.
+//
+// A workgroup computes BM activation rows x BN weight rows; its WX x WW waves share the tile,
+// each 16 * TX rows by 16 * TW weight rows of 16x16 MFMAs with the weight rows as A, so that a
+// lane's results run along an output row. K goes by in stages through a ring of D LDS buffers:
+//  - Loads go from memory straight into LDS (buffer_load ... lds), D - 1 stages ahead, with no
+//    registers in between. They are written as instructions without outputs, which the
+//    compiler does not wait for; one counted wait and one barrier per stage stand before its
+//    reads. Past the end of K (and of the rows) the loads are out of range and write zeros,
+//    so every stage issues the same number and the count holds to the last one.
+//  - A stage is 128 k of codes for MXFP4 activations (64 bytes a row on both sides), 64 k for
+//    BF16 ones (128 bytes of activations, 32 of codes).
+//  - LDS rows have no padding (the loads write 1 KiB runs); 16-byte piece q of a row lies at
+//    slot q ^ f(row), with f such that the 16 rows that lanes read together fall into
+//    different banks.
+//  - Weight row 4P * a + 4s + b of a group of 16P rows is row 4a + b of the MFMA of its s-th
+//    16-row tile (P tiles to a group): a lane's results are then 4P consecutive columns, so
+//    it stores 16 bytes at a time and holds a block's half or quarter when SwiGLU's result is
+//    quantized.
+#include "mx_device.hpp"
+#include "mx_kernels.hpp"
+
+namespace nvfp4 {
+namespace {
+
+constexpr uint32_t kOOB = 0x80000000u;
+
+__device__ __forceinline__ u32x4 make_rsrc(const void* base, int64_t bytes) {
+  const uint64_t p = (uint64_t)(uintptr_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32) & 0xFFFFu);
+  const uint32_t n = __builtin_amdgcn_readfirstlane((uint32_t)(bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes));
+  return u32x4{lo, hi, n, 0x00020000u};
+}
+
+// one load of BYTES bytes per lane into LDS: lane l's go to lds + l * max(BYTES, 4); lanes out
+// of the descriptor's range write zeros
+template <int BYTES>
+__device__ __forceinline__ void load_lds(u32x4 rsrc, uint32_t off, uint32_t lds) {
+  if (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+  else if (BYTES == 4)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_ubyte %0, %1, 0 offen lds"
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+}
+
+// all but this wave's latest N loads are done, its LDS reads too, and the other waves are here
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+template <int ACT_, int BM_, int BN_, int WX_, int WW_, int D_, bool BYTE_SCALES_>
+struct Shape {
+  static constexpr int ACT = ACT_, BM = BM_, BN = BN_, WX = WX_, WW = WW_, D = D_;
+  // MXFP4 activations: scales loaded one byte per lane (any K, any alignment), or one dword
+  // per row and stage (K % 128 == 0, dword-aligned scales)
+  static constexpr bool BYTE_SCALES = BYTE_SCALES_;
+  static constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
+  static constexpr int T = 64 * WX * WW;
+  static constexpr int TX = BM / WX / 16, TW = BN / WW / 16;
+  static constexpr int XB = MX ? 64 : 128, WB = MX ? 64 : 32;  // bytes of a row per stage
+  static constexpr int SB = MX ? 4 : 2;                        // weight blocks per stage
+  static constexpr int NX = BM * XB / (16 * T), NW = BN * WB / (16 * T);
+  // scale loads: BF16 activations BN * 2 bytes, one per lane; MXFP4 BM + BN rows
+  static constexpr int NS = !MX ? (BN * 2 + T - 1) / T
+                                : ((BM + BN) * (BYTE_SCALES ? 4 : 1) + T - 1) / T;
+  static constexpr int LOADS = NX + NW + NS;
+  static constexpr int X0 = 0, W0 = BM * XB, S0 = W0 + BN * WB, STAGE = S0 + NS * T * 4;
+  static constexpr int LDS = D * STAGE;
+  static_assert(NX * 16 * T == BM * XB && NW * 16 * T == BN * WB, "whole loads only");
+  static_assert(LDS <= 160 * 1024, "LDS");
+  static_assert(TW % 4 == 0, "weight rows come in groups of 64 (SwiGLU: 32 + 32)");
+};
+
+template <class S, bool GROUPED, int SWIGLU>
+__global__ __launch_bounds__(S::T) __attribute__((amdgpu_waves_per_eu(S::T == 512 ? 2 : 1, 2)))
+void mx_tiled(MxArgs a, int gm, int vec) {
+  constexpr int P = SWIGLU ? S::TW / 2 : 4;  // tiles of a group of weight rows
+  constexpr int GROUPS = S::TW / P;          // of a wave; SwiGLU: gate, up
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int wx = wave % S::WX, ww = wave / S::WX;
+  const int64_t N = a.N, K = a.K, half = N >> 1, nb = K >> 5;
+  const int64_t cols = SWIGLU ? half : N;
+  constexpr int BC = SWIGLU ? S::BN / 2 : S::BN;  // output columns of a tile
+  const int64_t nbn = (cols + BC - 1) / BC;
+
+  // tile of this workgroup: each XCD (blockIdx % 8) takes a run of tiles, which share
+  // operands through its L2
+  int64_t mt, nt;
+  {
+    const int64_t nbm = GROUPED ? *a.n_tiles : (a.M + S::BM - 1) / S::BM;
+    if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4) {
+      // scales of dropped routes, shared out over the launch (the grouping clears their codes)
+      const int64_t bytes = N >> 6;
+      for (int64_t r = (int64_t)blockIdx.x * S::T + tid; r < a.R; r += (int64_t)gridDim.x * S::T)
+        if (a.route_expert[r] < 0)
+          for (int64_t b = 0; b < bytes; b++) a.y_scales[r * bytes + b] = 0;
+    }
+    const int64_t total = nbm * nbn;
+    if (blockIdx.x >= total) return;
+    const int64_t q = total / 8, r = total % 8, x = blockIdx.x % 8;
+    const int64_t lin = x * q + (x < r ? x : r) + blockIdx.x / 8;
+    const int64_t first = lin / (gm * nbn) * gm, in = lin % (gm * nbn);
+    const int64_t rows = nbm - first < gm ? nbm - first : gm;
+    mt = first + in % rows;
+    nt = in / rows;
+  }
+  const int64_t n0 = nt * BC;
+  const uint8_t* wc = a.w_codes;
+  const uint8_t* ws = a.w_scales;
+  int64_t m0 = 0, rows_m;
+  int32_t slot0 = 0;
+  if (GROUPED) {
+    const int e = a.tiles[2 * mt];
+    slot0 = a.tiles[2 * mt + 1];
+    const int32_t left = a.offsets[e + 1] - slot0;
+    rows_m = left < S::BM ? left : S::BM;
+    wc += (int64_t)e * N * (K >> 1);
+    ws += (int64_t)e * N * nb;
+  } else {
+    m0 = mt * S::BM;
+    rows_m = a.M - m0 < S::BM ? a.M - m0 : S::BM;
+  }
+
+  // x row of tile row r (grouped: relative to x, dense: to the tile's first row)
+  const auto x_row = [&](int r) -> int64_t {
+    if (!GROUPED) return r;
+    const int32_t route = a.sorted[slot0 + r];
+    return a.rows_per_token ? route / a.top_k : route;
+  };
+  const int64_t xpitch = S::MX ? K >> 1 : a.ldx * 2;  // bytes
+  const int64_t x_last = GROUPED ? a.x_rows : rows_m;
+  const u32x4 xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (GROUPED ? 0 : m0 * xpitch),
+                             (x_last - 1) * xpitch + (S::MX ? K >> 1 : 2 * K));
+  const u32x4 wr = make_rsrc(wc + (SWIGLU ? 0 : n0 * (K >> 1)), (N - (SWIGLU ? 0 : n0)) * (K >> 1));
+  // weight row of tile row t relative to that base, or -1
+  const auto w_row = [&](int t) -> int64_t {
+    if (!SWIGLU) return n0 + t < N ? t : -1;
+    const int u = t >= BC ? t - BC : t;
+    return n0 + u < half ? n0 + u + (t >= BC ? half : 0) : -1;
+  };
+
+  // this lane's loads of stage 0; a stage on, offsets grow by XB / WB / SB bytes
+  uint32_t xo[S::NX], wo[S::NW], so[S::NS];
+  int xk[S::NX], wk[S::NW], sk[S::NS];  // first block (BF16 x: first 8-value piece) of the load
+#pragma unroll
+  for (int i = 0; i < S::NX; i++) {
+    const int p = i * S::T + tid;
+    const int r = S::MX ? p >> 2 : p >> 3;
+    const int q = S::MX ? (p & 3) ^ ((r >> 2) & 3) : (p & 7) ^ ((r >> 1) & 7);
+    xk[i] = q;
+    xo[i] = r < rows_m ? (uint32_t)(x_row(r) * xpitch) + 16 * q : kOOB;
+  }
+#pragma unroll
+  for (int i = 0; i < S::NW; i++) {
+    const int p = i * S::T + tid;
+    int t, q;
+    if (S::MX) {
+      t = p >> 2;
+      q = (p & 3) ^ ((t / (4 * P)) & 3);
+    } else {  // piece q of the row that lane p % 16 of 16-row tile p / 32 reads
+      const int u = p >> 5, s = u % P;
+      q = (p >> 4) & 1;
+      t = (u / P) * 16 * P + 4 * P * ((p & 15) >> 2) + 4 * s + (p & 3);
+    }
+    wk[i] = q;
+    const int64_t row = w_row(t);
+    wo[i] = row >= 0 ? (uint32_t)(row * (K >> 1)) + 16 * q : kOOB;
+  }
+  const u32x4 wsr = make_rsrc(ws + (SWIGLU ? 0 : n0 * nb), (N - (SWIGLU ? 0 : n0)) * nb);
+  const u32x4 xsr = S::MX ? make_rsrc(a.x_scales + (GROUPED ? 0 : m0 * nb), x_last * nb) : wsr;
+  // scale loads: p-th of the stage. BF16: weight row p / 2, block p % 2. MXFP4: rows of the
+  // weight, then of the activations, four blocks (one dword, or four byte loads) each. Whole
+  // waves read one side (BN is a multiple of 64), so the descriptor is uniform.
+  bool s_is_x[S::NS];
+#pragma unroll
+  for (int i = 0; i < S::NS; i++) {
+    const int p = i * S::T + tid;
+    const int per = !S::MX ? 2 : (S::BYTE_SCALES ? 4 : 1);
+    const int t = p / per;
+    sk[i] = p % per;
+    s_is_x[i] = S::MX && __builtin_amdgcn_readfirstlane(t) >= S::BN;
+    int64_t row = -1;
+    if (t < S::BN) row = w_row(t);
+    else if (S::MX && t - S::BN < rows_m) row = x_row(t - S::BN);
+    so[i] = row >= 0 ? (uint32_t)(row * nb) + sk[i] : kOOB;
+  }
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  const int nblk = (int)nb;
+  const auto issue = [&](int st, int buf) {
+    const uint32_t base = lds0 + buf * S::STAGE;
+#pragma unroll
+    for (int i = 0; i < S::NX; i++) {
+      // a BF16 piece is in range when its block is: pieces 4 per block
+      const int b = S::MX ? 4 * st + xk[i] : 2 * st + (xk[i] >> 2);
+      load_lds<16>(xr, b < nblk ? xo[i] + st * S::XB : kOOB, base + S::X0 + (i * S::T + wave * 64) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < S::NW; i++)
+      load_lds<16>(wr, S::SB * st + wk[i] < nblk ? wo[i] + st * S::WB : kOOB,
+                   base + S::W0 + (i * S::T + wave * 64) * 16);
+#pragma unroll
+    for (int i = 0; i < S::NS; i++) {
+      const uint32_t off = S::SB * st + sk[i] < nblk ? so[i] + st * S::SB : kOOB;
+      load_lds<(S::MX && !S::BYTE_SCALES) ? 4 : 1>(s_is_x[i] ? xsr : wsr, off,
+                                                   base + S::S0 + (i * S::T + wave * 64) * 4);
+    }
+  };
+
+  f32x4 acc[S::TW][S::TX];
+#pragma unroll
+  for (int t = 0; t < S::TW; t++)
+#pragma unroll
+    for (int x = 0; x < S::TX; x++) acc[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // tile row of MFMA row 4a + b of this wave's weight tile t
+  const auto w_local = [&](int t, int row) {
+    const int grp = t / P, s = t % P;
+    const int base = SWIGLU ? grp * BC + ww * 16 * P : (ww * GROUPS + grp) * 16 * P;
+    return base + 4 * P * (row >> 2) + 4 * s + (row & 3);
+  };
+
+  const int steps = (nblk + S::SB - 1) / S::SB;
+#pragma unroll
+  for (int i = 0; i < S::D - 1; i++) issue(i, i);
+  int buf = 0;
+  for (int st = 0; st < steps; st++) {
+    wait_barrier<(S::D - 2) * S::LOADS>();
+    issue(st + S::D - 1, buf == 0 ? S::D - 1 : buf - 1);
+    const uint8_t* xs = smem + buf * S::STAGE + S::X0;
+    const uint8_t* wl = smem + buf * S::STAGE + S::W0;
+    const uint8_t* sl = smem + buf * S::STAGE + S::S0;
+    if (S::MX) {
+      u32x4 xf[S::TX];
+      uint32_t xsc[S::TX];
+#pragma unroll
+      for (int x = 0; x < S::TX; x++) {
+        const int r = (wx * S::TX + x) * 16 + c;
+        xf[x] = *reinterpret_cast<const u32x4*>(xs + r * 64 + ((g ^ ((r >> 2) & 3)) << 4));
+        xsc[x] = S::BYTE_SCALES ? sl[((S::BN + r) * 4 + g) * 4] : sl[(S::BN + r) * 4 + g];
+      }
+#pragma unroll
+      for (int t = 0; t < S::TW; t++) {
+        const int r = w_local(t, c);
+        const u32x4 wf = *reinterpret_cast<const u32x4*>(wl + r * 64 + ((g ^ ((r / (4 * P)) & 3)) << 4));
+        const uint32_t s = S::BYTE_SCALES ? sl[(r * 4 + g) * 4] : sl[r * 4 + g];
+#pragma unroll
+        for (int x = 0; x < S::TX; x++) acc[t][x] = mfma_mx(wf, xf[x], acc[t][x], s, xsc[x]);
+      }
+    } else {
+      u32x4 xf[S::TX][2];
+#pragma unroll
+      for (int x = 0; x < S::TX; x++) {
+        const int r = (wx * S::TX + x) * 16 + c;
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+          xf[x][j] = *reinterpret_cast<const u32x4*>(xs + r * 128 + (((2 * g + j) ^ ((r >> 1) & 7)) << 4));
+      }
+#pragma unroll
+      for (int t = 0; t < S::TW; t++) {
+        const int r = w_local(t, c);
+        // 16-row tile index in the order of the loads
+        const int u = (r / (16 * P)) * P + (t % P);
+        const uint2 w = *reinterpret_cast<const uint2*>(wl + u * 512 + (((g >> 1) * 16 + c) << 4) + ((g & 1) << 3));
+        const float s = e8m0_operand(sl[(r * 2 + (g >> 1)) * 4]);
+        const u32x4 w0 = mx_decode8(w.x, s), w1 = mx_decode8(w.y, s);
+#pragma unroll
+        for (int x = 0; x < S::TX; x++) acc[t][x] = mfma16(w0, xf[x][0], acc[t][x]);
+#pragma unroll
+        for (int x = 0; x < S::TX; x++) acc[t][x] = mfma16(w1, xf[x][1], acc[t][x]);
+      }
+    }
+    buf = buf + 1 == S::D ? 0 : buf + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing writes LDS after the workgroup
+
+#pragma unroll
+  for (int x = 0; x < S::TX; x++) {
+    const int r = (wx * S::TX + x) * 16 + c;
+    const bool ok = r < rows_m;
+    const int64_t row = GROUPED ? (ok ? a.sorted[slot0 + r] : 0) : m0 + r;
+    if (!SWIGLU) {
+#pragma unroll
+      for (int grp = 0; grp < GROUPS; grp++) {
+        const int64_t n = n0 + w_local(grp * P, 4 * g);
+        if (!ok) continue;
+        if (vec && n + 4 * P <= N) {
+          if (a.y_type == MXFP4_F32) {
+            f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + row * a.ldy + n);
+#pragma unroll
+            for (int s = 0; s < P; s++) d[s] = acc[grp * P + s][x];
+          } else {
+            u32x4* d = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.y) + row * a.ldy + n);
+#pragma unroll
+            for (int s = 0; s < P; s += 2) {
+              const f32x4 u = acc[grp * P + s][x], v = acc[grp * P + s + 1][x];
+              d[s / 2] = u32x4{bf16_pair(u[0], u[1]), bf16_pair(u[2], u[3]), bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+            }
+          }
+          continue;
+        }
+#pragma unroll
+        for (int s = 0; s < P; s++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            if (n + 4 * s + i >= N) continue;
+            const float v = acc[grp * P + s][x][i];
+            if (a.y_type == MXFP4_F32)
+              static_cast<float*>(a.y)[row * a.ldy + n + 4 * s + i] = v;
+            else
+              static_cast<uint16_t*>(a.y)[row * a.ldy + n + 4 * s + i] = (uint16_t)bf16_pair(v, 0.f);
+          }
+      }
+      continue;
+    }
+    // SwiGLU: tile t and tile P + t are gate and up of the same columns
+    const int64_t n = n0 + w_local(0, 4 * g);
+    uint32_t h[2 * P];  // BF16 pairs of 4P consecutive columns
+#pragma unroll
+    for (int s = 0; s < P; s++) {
+      const f32x4 gt = acc[s][x], u = acc[P + s][x];
+      h[2 * s] = bf16_pair(silu(gt[0]) * u[0], silu(gt[1]) * u[1]);
+      h[2 * s + 1] = bf16_pair(silu(gt[2]) * u[2], silu(gt[3]) * u[3]);
+    }
+    if (SWIGLU == MXFP4_OUT_SWIGLU_BF16) {
+      if (!ok) continue;
+      uint16_t* d = static_cast<uint16_t*>(a.y) + row * half + n;
+      if (vec && n + 4 * P <= half) {
+#pragma unroll
+        for (int s = 0; s < P / 2; s++)
+          reinterpret_cast<u32x4*>(d)[s] = u32x4{h[4 * s], h[4 * s + 1], h[4 * s + 2], h[4 * s + 3]};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4 * P; i++)
+          if (n + i < half) d[i] = (uint16_t)(h[i >> 1] >> (16 * (i & 1)));
+      }
+      continue;
+    }
+    uint32_t amax = 0u;
+#pragma unroll
+    for (int i = 0; i < 2 * P; i++) {
+      const uint32_t lo = (h[i] & 0x7FFFu) << 16, hi = h[i] & 0x7FFF0000u;
+      amax = amax > lo ? amax : lo;
+      amax = amax > hi ? amax : hi;
+    }
+    uint32_t o = __shfl_xor(amax, 16, 64);
+    amax = amax > o ? amax : o;
+    if (P == 2) {
+      o = __shfl_xor(amax, 32, 64);
+      amax = amax > o ? amax : o;
+    }
+    const uint32_t sc = e8m0_of_amax(amax);
+    const bool bad = amax >= 0x7F800000u;
+    uint32_t code[P / 2];
+#pragma unroll
+    for (int i = 0; i < P / 2; i++) {
+      float q[8];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        q[2 * j] = __builtin_ldexpf(__uint_as_float(h[4 * i + j] << 16), 127 - (int)sc);
+        q[2 * j + 1] = __builtin_ldexpf(__uint_as_float(h[4 * i + j] & 0xFFFF0000u), 127 - (int)sc);
+      }
+      uint32_t v = e2m1_rne2<0>(0u, q[0], q[1]);
+      v = e2m1_rne2<1>(v, q[2], q[3]);
+      v = e2m1_rne2<2>(v, q[4], q[5]);
+      v = e2m1_rne2<3>(v, q[6], q[7]);
+      code[i] = bad ? 0u : v;
+    }
+    if (!ok || n >= half) continue;  // blocks end where the columns do
+    uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + row * (half >> 1) + (n >> 1));
+#pragma unroll
+    for (int i = 0; i < P / 2; i++) d[i] = code[i];
+    if ((n & 31) == 0) a.y_scales[row * (half >> 5) + (n >> 5)] = (uint8_t)(bad ? kE8M0Nan : sc);
+  }
+}
+
+template <class S>
+hipError_t launch_shape(const MxArgs& a, int64_t max_tiles, hipStream_t stream) {
+  const int64_t bc = a.swiglu ? S::BN / 2 : S::BN;
+  const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
+  const int64_t nbm = a.tiles ? max_tiles : (a.M + S::BM - 1) / S::BM;
+  const int64_t groups = nbm * ((cols + bc - 1) / bc);
+  if (groups * S::T > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
+  const int gm = S::MX ? 4 : 2;
+  const int64_t ysz = a.y_type == MXFP4_F32 ? 4 : 2, ld = a.swiglu ? cols : a.ldy;
+  const int vec = ((uintptr_t)a.y | (uintptr_t)(ld * ysz)) % 16 == 0;
+  auto k = !a.tiles ? mx_tiled<S, false, 0>
+           : a.swiglu == 0 ? mx_tiled<S, true, 0>
+           : a.swiglu == MXFP4_OUT_SWIGLU_BF16 ? mx_tiled<S, true, MXFP4_OUT_SWIGLU_BF16>
+                                               : mx_tiled<S, true, MXFP4_OUT_SWIGLU_MXFP4>;
+  hipLaunchKernelGGL(k, dim3((uint32_t)groups), dim3(S::T), S::LDS, stream, a, a.tiles ? 1 : gm, vec);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool mx_tiled_takes(const MxArgs& a, int act_kind) {
+  // 32-bit offsets into the activations (dense: from the tile's first row) and one weight
+  const int64_t pitch = act_kind == MXFP4_ACT_MXFP4 ? a.K >> 1 : a.ldx * 2;
+  const int64_t rows = a.tiles ? a.x_rows : (a.M < 256 ? a.M : 256);
+  return rows * pitch < (int64_t)kOOB && a.N * (a.K >> 1) < (int64_t)kOOB;
+}
+
+hipError_t launch_mx_tiled(const MxArgs& a, int act_kind, int64_t max_tiles, hipStream_t stream) {
+  const bool wide = !a.tiles;
+  if (act_kind == MXFP4_ACT_BF16) {
+    if (wide) return launch_shape<Shape<MXFP4_ACT_BF16, 256, 256, 4, 2, 3, false>>(a, max_tiles, stream);
+    return launch_shape<Shape<MXFP4_ACT_BF16, 128, 256, 4, 2, 4, false>>(a, max_tiles, stream);
+  }
+  const bool dwords = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.w_scales) % 4 == 0;
+  if (wide) {
+    if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 256, 256, 2, 4, 4, false>>(a, max_tiles, stream);
+    return launch_shape<Shape<MXFP4_ACT_MXFP4, 256, 256, 2, 4, 3, true>>(a, max_tiles, stream);
+  }
+  if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 128, 256, 2, 4, 4, false>>(a, max_tiles, stream);
+  return launch_shape<Shape<MXFP4_ACT_MXFP4, 128, 256, 2, 4, 4, true>>(a, max_tiles, stream);
+}
+
+}  // namespace nvfp4
