@@ -143,9 +143,9 @@ nvfp4_status mxfp4_linear(int32_t act_kind, const void* x, const uint8_t* x_scal
   MxArgs a{};
   a.x = x; a.x_scales = x_scales; a.ldx = ldx;
   a.w_codes = w_codes; a.w_scales = w_scales;
-  a.M = M; a.N = N; a.K = K;
+  a.M = a.x_rows = M; a.N = N; a.K = K;
   a.y = y; a.ldy = ldy; a.y_type = y_type;
-  return launch_status(launch_mx_product(a, act_kind, 0, s));
+  return launch_status(launch_mx_product(a, act_kind, 0, 0, s));
 }
 
 nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t* x_scales,
@@ -229,6 +229,7 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
   a.w_codes = w_codes; a.w_scales = w_scales;
   a.N = N; a.K = K;
   a.tiles = ws.tiles; a.n_tiles = ws.n_tiles; a.offsets = ws.offsets; a.sorted = ws.sorted;
+  a.slots = ws.slots;
   a.route_expert = ws.route_expert; a.R = R;
   a.tile_rows = L.tile_rows;
   a.x_rows = rows_mode == NVFP4_ROWS_PER_TOKEN ? T : R;
@@ -240,7 +241,7 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
     a.y = rows;
     a.y_type = MXFP4_F32;
   }
-  hipError_t e = launch_mx_product(a, act_kind, L.max_tiles, s);
+  hipError_t e = launch_mx_product(a, act_kind, L.max_tiles, ws.max_slots, s);
   if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
   if (out_mode == MXFP4_OUT_COMBINE)
     e = launch_mx_combine(rows, ws.route_expert, topk_w, T, top_k, N, y_type, y, s);

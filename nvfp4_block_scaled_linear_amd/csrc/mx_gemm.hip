@@ -175,9 +175,14 @@ __global__ __launch_bounds__(64) void mx_tile(MxArgs a) {
 
 int mx_tile_rows(int64_t R, int64_t active) { return R >= 64 * active ? 128 : kTileRows; }
 
-hipError_t launch_mx_product(const MxArgs& a, int act_kind, int64_t max_tiles, hipStream_t stream) {
-  if ((a.tiles ? a.tile_rows > kTileRows : a.M >= 64) && mx_tiled_takes(a, act_kind))
-    return launch_mx_tiled(a, act_kind, max_tiles, stream);
+hipError_t launch_mx_product(const MxArgs& a, int act_kind, int64_t max_tiles, int64_t max_slots,
+                             hipStream_t stream) {
+  if (a.tiles ? a.tile_rows > kTileRows : a.M > 64) {
+    if (mx_tiled_takes(a, act_kind)) return launch_mx_tiled(a, act_kind, max_tiles, stream);
+  } else if (mx_stream_takes(a, act_kind)) {
+    const int64_t rows = a.tiles ? (a.R + max_slots - 1) / max_slots : a.M;
+    return launch_mx_stream(a, act_kind, rows, max_slots, stream);
+  }
   const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
   const int64_t gx = a.tiles ? max_tiles * (a.tile_rows / kTileRows) : (a.M + kTileRows - 1) / kTileRows;
   const int64_t groups = gx * ((cols + kTileCols - 1) / kTileCols);

@@ -31,6 +31,7 @@ struct MxArgs {
   int64_t x_rows;          // rows of x
   const int32_t* tiles;    // [n_tiles][2] (expert, first slot in sorted)
   const int32_t* n_tiles;  // [1]
+  const int32_t* slots;    // [max_slots] slot records (RouteWorkspace::slots)
   const int32_t* offsets;  // [E+1]
   const int32_t* sorted;   // route ids grouped by expert
   const int32_t* route_expert;  // [R] expert of a route, -1 when dropped
@@ -50,8 +51,14 @@ int mx_tile_rows(int64_t R, int64_t active);
 // the kernel for LDS tiles (mx_tiled.hip), and whether its 32-bit offsets reach the operands
 bool mx_tiled_takes(const MxArgs& a, int act_kind);
 hipError_t launch_mx_tiled(const MxArgs& a, int act_kind, int64_t max_tiles, hipStream_t stream);
-// max_tiles bounds the tile list of the grouped form (0: dense)
-hipError_t launch_mx_product(const MxArgs& a, int act_kind, int64_t max_tiles, hipStream_t stream);
+// the kernel that streams the weight (mx_stream.hip) for about `rows` activation rows per
+// weight (dense: M of them, at most 64)
+bool mx_stream_takes(const MxArgs& a, int act_kind);
+hipError_t launch_mx_stream(const MxArgs& a, int act_kind, int64_t rows, int64_t max_slots,
+                            hipStream_t stream);
+// max_tiles and max_slots bound the tile list and the slot records of the grouped form (0: dense)
+hipError_t launch_mx_product(const MxArgs& a, int act_kind, int64_t max_tiles, int64_t max_slots,
+                             hipStream_t stream);
 
 // y[t] = sum over t's kept routes in ascending expert id of topk_w * rows[route]
 hipError_t launch_mx_combine(const float* rows, const int32_t* route_expert, const float* topk_w,
