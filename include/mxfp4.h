@@ -11,7 +11,9 @@
  *   codes   [N][K/2]  uint8, byte j of a row holds k = 2j in its low nibble and
  *                      k = 2j+1 in its high nibble; rows contiguous, base 16-byte aligned;
  *   scales  [N][K/32] uint8, any alignment.
- * K % 32 == 0; M, N and T may be any positive size.
+ * K % 32 == 0; M, N and T may be any positive size up to 2^22, K likewise. Offsets into
+ * the activations (of a dense call: into 256 rows of them) and into one expert's codes are
+ * 32-bit: 2^31 bytes and more are refused (NVFP4_ERR_SHAPE).
  *
  * Ownership, streams, argument errors, faults and determinism are as stated in nvfp4.h:
  * nothing is allocated or synchronized, bad arguments are refused on the host before

@@ -19,35 +19,32 @@ MX_EXPORTS = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_group
 _ACT_BF16, _ACT_MXFP4 = 0, 1
 _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 _TYPES = {_BF16: 0, _F32: 1}
-_fns = None
+_lib = None
 # the current stream's handle of a device (torch.cuda.current_stream(i).cuda_stream without the
 # Stream object, which costs as much as the rest of a call's host work)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _load():
-    """The entry points by name, with their argument types."""
-    global _fns
-    if _fns is None:
+    """The library, the argument types of these entry points set."""
+    global _lib
+    if _lib is None:
         lib = _binding.load_library()
         vp, i64, i32, u32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32
-        args = {
-            "mxfp4_quantize": [i32, vp, i64, i64, i64, vp, vp, vp, vp],
-            "mxfp4_dequantize": [vp, vp, i64, i64, i32, vp, i64, vp],
-            "mxfp4_linear": [i32, vp, vp, i64, i64, i64, i64, vp, vp, i32, vp, i64, u32, vp, vp],
-            "mxfp4_grouped_linear": [i32, vp, vp, i64, i32, i64, i32, i64, i64, i32, vp, vp, vp, vp, i32, i32, vp, vp,
-                                     vp, ctypes.POINTER(ctypes.c_size_t), u32, vp, vp],
-        }
-        for name, types in args.items():
-            fn = getattr(lib, name)
-            fn.argtypes, fn.restype = types, i32
-        _fns = {name: getattr(lib, name) for name in args}
-    return _fns
+        lib.mxfp4_quantize.argtypes = [i32, vp, i64, i64, i64, vp, vp, vp, vp]
+        lib.mxfp4_dequantize.argtypes = [vp, vp, i64, i64, i32, vp, i64, vp]
+        lib.mxfp4_linear.argtypes = [i32, vp, vp, i64, i64, i64, i64, vp, vp, i32, vp, i64, u32, vp, vp]
+        lib.mxfp4_grouped_linear.argtypes = [i32, vp, vp, i64, i32, i64, i32, i64, i64, i32, vp, vp, vp, vp, i32, i32,
+                                             vp, vp, vp, ctypes.POINTER(ctypes.c_size_t), u32, vp, vp]
+        for name in MX_EXPORTS:
+            getattr(lib, name).restype = i32
+        _lib = lib
+    return _lib
 
 
 def _run(device, name, *args):
     """Calls the entry point `name` on `device`'s current stream."""
-    fn = (_fns or _load())[name]
+    fn = getattr(_lib or _load(), name)
     stream = _raw_stream(device.index)
     if device.index == torch.cuda.current_device():
         st = fn(*args, stream)
@@ -175,7 +172,7 @@ def mxfp4_linear(x, w_codes, w_scales, *, x_scales=None, out=None, out_dtype=_F3
 def mxfp4_grouped_workspace_size(T: int, top_k: int, N: int, K: int, num_experts: int, out_mode: int) -> int:
     """Bytes of workspace that mxfp4_grouped_linear needs for these sizes."""
     n = ctypes.c_size_t(0)
-    st = _load()["mxfp4_grouped_linear"](_ACT_BF16, None, None, K, 0, T, top_k, N, K, num_experts, None, None, None,
+    st = (_lib or _load()).mxfp4_grouped_linear(_ACT_BF16, None, None, K, 0, T, top_k, N, K, num_experts, None, None, None,
                                          None, out_mode, 0, None, None, None, ctypes.byref(n), 0, None, None)
     if st:
         _check(st, "mxfp4_grouped_linear (workspace query)")

@@ -58,34 +58,66 @@ hipError_t check_data(int32_t act_kind, const void* x, const uint8_t* x_scales, 
                                      : launch_check_bf16(x, ldx, rows, K, faults, s);
 }
 
+// The kernels address activation rows and one expert's weight with 32-bit buffer offsets.
+bool fits(int64_t rows, int64_t pitch_bytes) { return rows * pitch_bytes < (int64_t)1 << 31; }
+
+int64_t x_pitch(int32_t act_kind, int64_t ldx, int64_t K) {
+  return act_kind == MXFP4_ACT_MXFP4 ? K / 2 : ldx * 2;
+}
+
+// How the grouped call goes about R = T * top_k routes. It depends on nothing else, so that
+// both calls of a layer agree on the workspace's grouping.
+//  - scan: few routes; each workgroup looks for its expert in topk_ids and nothing is grouped.
+//  - slots: less than kTiledRoutes routes per active expert on average; the weight is
+//    streamed for up to 16 routes, experts with more have the rest in the list of tiles.
+//  - tiles of 64 or 128 routes for more.
+constexpr int64_t kStreamRows = 64;   // dense: rows that the streaming kernel takes
+constexpr int64_t kTiledRoutes = 16;
+constexpr int64_t kTile128Routes = 96;
+
+struct Plan {
+  bool scan, slots;
+  int tile_rows, main_rows;
+  int64_t max_tiles;
+};
+
+Plan plan_of(int64_t T, int top_k, int E) {
+  const int64_t R = T * top_k, active = R < E ? R : E;
+  if (R < kTiledRoutes * active) {
+    // an expert has at most T routes; past its first 16, c routes make at most c / 16 tiles
+    if (R <= mx_scan_routes()) return {true, false, 0, 0, 0};
+    return {false, true, kMxSlotRoutes, kMxSlotRoutes, T > kMxSlotRoutes ? R / kMxSlotRoutes : 0};
+  }
+  const int rows = R < kTile128Routes * active ? 64 : 128;
+  return {false, false, rows, 0, R / rows + active};  // one partial tile per expert
+}
+
 // grouped-call workspace: 256-byte aligned regions, those of the grouping first and the same
 // in every output form
 struct Layout {
   size_t offsets, active, n_active, route_expert, sorted, slots, tiles, n_tiles, chunks, rows, total;
-  int64_t max_tiles;
-  int tile_rows;
 };
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-Layout mx_layout(int64_t T, int top_k, int E, int64_t N, int32_t out_mode) {
-  Layout L;
+Layout layout_of(const Plan& p, int64_t T, int top_k, int E, int64_t N, int32_t out_mode) {
+  Layout L{};
   const int64_t R = T * top_k, active = R < E ? R : E;
-  L.tile_rows = mx_tile_rows(R, active);
-  L.max_tiles = (R + L.tile_rows - 1) / L.tile_rows + active;  // one partial tile per expert
-  size_t o = 0;
-  const auto region = [&o](size_t ints) { const size_t at = o; o = up256(o + 4 * ints); return at; };
-  L.offsets = region((size_t)E + 1);
-  L.active = region((size_t)E);
-  L.n_active = region(1);
-  L.route_expert = region((size_t)R);
-  L.sorted = region((size_t)R);
-  L.slots = region((size_t)kSlotInts * (size_t)active);
-  L.tiles = region(2 * (size_t)L.max_tiles);
-  L.n_tiles = region(1);
-  L.chunks = region((size_t)route_chunk_ints(T, top_k, E));
+  size_t o = 256;  // never empty
+  const auto region = [&o](int64_t ints) { const size_t at = o; o = up256(o + 4 * (size_t)ints); return at; };
+  if (!p.scan) {
+    L.offsets = region(E + 1);
+    L.active = region(E);
+    L.n_active = region(1);
+    L.route_expert = region(R);
+    L.sorted = region(R);
+    L.slots = region(kSlotInts * active);
+    L.tiles = region(2 * p.max_tiles);
+    L.n_tiles = region(1);
+    L.chunks = region(route_chunk_ints(T, top_k, E));
+  }
   L.rows = o;
-  if (out_mode == MXFP4_OUT_COMBINE) region((size_t)R * (size_t)N);
+  if (out_mode == MXFP4_OUT_COMBINE) region(R * N);
   L.total = o;
   return L;
 }
@@ -134,6 +166,7 @@ nvfp4_status mxfp4_linear(int32_t act_kind, const void* x, const uint8_t* x_scal
   if (!y) return NVFP4_ERR_NULL;
   if (ldy < N || ldy > kMaxDim) return NVFP4_ERR_SHAPE;
   if (!aligned(y, (uintptr_t)type_bytes(y_type))) return NVFP4_ERR_ALIGN;
+  if (!fits(M < 256 ? M : 256, x_pitch(act_kind, ldx, K))) return NVFP4_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (flags & NVFP4_F_CHECK) {
     const hipError_t e =
@@ -145,7 +178,7 @@ nvfp4_status mxfp4_linear(int32_t act_kind, const void* x, const uint8_t* x_scal
   a.w_codes = w_codes; a.w_scales = w_scales;
   a.M = a.x_rows = M; a.N = N; a.K = K;
   a.y = y; a.ldy = ldy; a.y_type = y_type;
-  return launch_status(launch_mx_product(a, act_kind, 0, 0, s));
+  return launch_status(M <= kStreamRows ? launch_mx_stream(a, act_kind, M, s) : launch_mx_tiled(a, act_kind, s));
 }
 
 nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t* x_scales,
@@ -174,7 +207,9 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
     return NVFP4_ERR_SHAPE;
   if (out_mode == MXFP4_OUT_SWIGLU_BF16 && N % 2 != 0) return NVFP4_ERR_SHAPE;
   if (out_mode == MXFP4_OUT_SWIGLU_MXFP4 && N % 64 != 0) return NVFP4_ERR_SHAPE;
-  const Layout L = mx_layout(T, top_k, num_experts, N, out_mode);
+  if (!fits(N, K / 2)) return NVFP4_ERR_SHAPE;
+  const Plan plan = plan_of(T, top_k, num_experts);
+  const Layout L = layout_of(plan, T, top_k, num_experts, N, out_mode);
   if (!workspace) {
     *workspace_bytes = L.total;
     return NVFP4_OK;
@@ -191,60 +226,65 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
   if (!aligned(y, out_mode == MXFP4_OUT_SWIGLU_MXFP4 ? 16 : (uintptr_t)type_bytes(y_type)))
     return NVFP4_ERR_ALIGN;
 
+  const int64_t R = T * top_k, xrows = rows_mode == NVFP4_ROWS_PER_TOKEN ? T : R;
+  if (!fits(xrows, x_pitch(act_kind, ldx, K))) return NVFP4_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t R = T * top_k;
   if (flags & NVFP4_F_CHECK) {
-    const int64_t xrows = rows_mode == NVFP4_ROWS_PER_TOKEN ? T : R;
     const hipError_t e = check_data(act_kind, x, x_scales, ldx, xrows, K, w_scales,
                                     (int64_t)num_experts * N * (K / 32), faults, s);
     if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
   }
   char* base = static_cast<char*>(workspace);
   const auto ints = [base](size_t at) { return reinterpret_cast<int32_t*>(base + at); };
-  RouteWorkspace ws{};
-  ws.offsets = ints(L.offsets);
-  ws.active = ints(L.active);
-  ws.n_active = ints(L.n_active);
-  ws.route_expert = ints(L.route_expert);
-  ws.sorted = ints(L.sorted);
-  ws.slots = ints(L.slots);
-  ws.max_slots = (int32_t)(R < num_experts ? R : num_experts);
-  ws.tiles = ints(L.tiles);
-  ws.n_tiles = ints(L.n_tiles);
-  ws.chunk_counts = ints(L.chunks);
-  ws.tile_rows = L.tile_rows;
-  ws.main_rows = 0;
   float* rows = reinterpret_cast<float*>(base + L.rows);
-  if (!reuse) {
-    // the grouping clears the rows of dropped routes (MXFP4: their codes)
-    const bool keep = out_mode == MXFP4_OUT_COMBINE;
-    const int64_t row_bytes = out_mode == MXFP4_OUT_ROUTES ? N * type_bytes(y_type)
-                              : out_mode == MXFP4_OUT_SWIGLU_BF16 ? N : N / 4;
-    const hipError_t e = launch_route_sort(topk_ids, T, top_k, num_experts, ws, faults,
-                                           keep ? nullptr : y, row_bytes, s);
-    if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
-  }
   MxArgs a{};
   a.x = x; a.x_scales = x_scales; a.ldx = ldx;
   a.w_codes = w_codes; a.w_scales = w_scales;
   a.N = N; a.K = K;
-  a.tiles = ws.tiles; a.n_tiles = ws.n_tiles; a.offsets = ws.offsets; a.sorted = ws.sorted;
-  a.slots = ws.slots;
-  a.route_expert = ws.route_expert; a.R = R;
-  a.tile_rows = L.tile_rows;
-  a.x_rows = rows_mode == NVFP4_ROWS_PER_TOKEN ? T : R;
-  a.rows_per_token = rows_mode == NVFP4_ROWS_PER_TOKEN ? 1 : 0;
-  a.top_k = top_k;
+  a.R = R; a.x_rows = xrows; a.rows_per_token = rows_mode == NVFP4_ROWS_PER_TOKEN ? 1 : 0;
+  a.top_k = top_k; a.num_experts = num_experts;
   a.y = y; a.y_scales = y_scales; a.ldy = N; a.y_type = y_type;
   a.swiglu = swiglu ? out_mode : 0;
   if (out_mode == MXFP4_OUT_COMBINE) {
     a.y = rows;
     a.y_type = MXFP4_F32;
   }
-  hipError_t e = launch_mx_product(a, act_kind, L.max_tiles, ws.max_slots, s);
+  hipError_t e = hipSuccess;
+  if (plan.scan) {
+    a.ids = topk_ids;
+    a.faults = reuse ? nullptr : faults;  // reported by the earlier call
+  } else {
+    RouteWorkspace ws{};
+    ws.offsets = ints(L.offsets);
+    ws.active = ints(L.active);
+    ws.n_active = ints(L.n_active);
+    ws.route_expert = ints(L.route_expert);
+    ws.sorted = ints(L.sorted);
+    ws.slots = ints(L.slots);
+    ws.max_slots = (int32_t)(R < num_experts ? R : num_experts);
+    ws.tiles = ints(L.tiles);
+    ws.n_tiles = ints(L.n_tiles);
+    ws.chunk_counts = ints(L.chunks);
+    ws.tile_rows = plan.tile_rows;
+    ws.main_rows = plan.main_rows;
+    if (!reuse) {
+      // the grouping clears the rows of dropped routes (MXFP4: their codes)
+      const bool keep = out_mode == MXFP4_OUT_COMBINE;
+      const int64_t row_bytes = out_mode == MXFP4_OUT_ROUTES ? N * type_bytes(y_type)
+                                : out_mode == MXFP4_OUT_SWIGLU_BF16 ? N : N / 4;
+      e = launch_route_sort(topk_ids, T, top_k, num_experts, ws, faults, keep ? nullptr : y,
+                            row_bytes, s);
+      if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
+    }
+    a.tile_rows = plan.tile_rows; a.max_tiles = plan.max_tiles; a.max_slots = ws.max_slots;
+    a.tiles = ws.tiles; a.n_tiles = ws.n_tiles; a.offsets = ws.offsets; a.sorted = ws.sorted;
+    a.slots = ws.slots; a.route_expert = ws.route_expert;
+  }
+  e = plan.scan || plan.slots ? launch_mx_stream(a, act_kind, (R + num_experts - 1) / num_experts, s)
+                              : launch_mx_tiled(a, act_kind, s);
   if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
   if (out_mode == MXFP4_OUT_COMBINE)
-    e = launch_mx_combine(rows, ws.route_expert, topk_w, T, top_k, N, y_type, y, s);
+    e = launch_mx_combine(rows, topk_ids, topk_w, T, top_k, num_experts, N, y_type, y, s);
   return launch_status(e);
 }
 

@@ -9,28 +9,38 @@ constexpr int kThreads = 256;
 constexpr int kMaxTopK = 64;
 
 // One workgroup per (token, 1024 columns). The first top_k threads rank their routes by
-// expert among the token's kept ones (ids are distinct within a token) and stage row and
+// expert among the token's kept ones (in range, the first of their id) and stage row and
 // weight in that order; each thread then adds its four columns of the rows with fmaf, in
 // that order, from zero.
 __global__ __launch_bounds__(kThreads) void mx_combine(const float* rows,
-                                                       const int32_t* route_expert,
-                                                       const float* topk_w, int top_k, int64_t N,
-                                                       int y_type, void* y) {
+                                                       const int32_t* topk_ids,
+                                                       const float* topk_w, int top_k, int E,
+                                                       int64_t N, int y_type, void* y) {
   __shared__ int32_t ex[kMaxTopK];
   __shared__ int64_t rr[kMaxTopK];
   __shared__ float wr[kMaxTopK];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x;
   int32_t e = -1;
-  if (tid < top_k) ex[tid] = e = route_expert[t * top_k + tid];
+  float w = 0.f;
+  if (tid < top_k) {
+    ex[tid] = e = topk_ids[t * top_k + tid];
+    w = topk_w[t * top_k + tid];
+  }
   __syncthreads();
-  int kept = 0;
-  for (int j = 0; j < top_k; j++) kept += ex[j] >= 0;
-  if (e >= 0) {
-    int slot = 0;
-    for (int j = 0; j < top_k; j++) slot += ex[j] >= 0 && ex[j] < e;
+  int kept = 0, slot = 0;
+  bool mine = e >= 0 && e < E;
+  for (int j = 0; j < top_k; j++) {
+    const int32_t f = ex[j];
+    bool ok = f >= 0 && f < E;
+    for (int i = 0; i < j; i++) ok = ok && ex[i] != f;
+    kept += ok;
+    slot += ok && f < e;
+    if (j < tid && f == e) mine = false;
+  }
+  if (mine) {
     rr[slot] = t * top_k + tid;
-    wr[slot] = topk_w[t * top_k + tid];
+    wr[slot] = w;
   }
   __syncthreads();
   const int64_t n0 = (int64_t)blockIdx.y * (4 * kThreads) + 4 * tid;
@@ -72,11 +82,11 @@ __global__ __launch_bounds__(kThreads) void mx_combine(const float* rows,
 
 }  // namespace
 
-hipError_t launch_mx_combine(const float* rows, const int32_t* route_expert, const float* topk_w,
-                             int64_t T, int top_k, int64_t N, int y_type, void* y,
+hipError_t launch_mx_combine(const float* rows, const int32_t* topk_ids, const float* topk_w,
+                             int64_t T, int top_k, int E, int64_t N, int y_type, void* y,
                              hipStream_t stream) {
   hipLaunchKernelGGL(mx_combine, dim3((uint32_t)T, (uint32_t)((N + 4 * kThreads - 1) / (4 * kThreads))),
-                     dim3(kThreads), 0, stream, rows, route_expert, topk_w, top_k, N, y_type, y);
+                     dim3(kThreads), 0, stream, rows, topk_ids, topk_w, top_k, E, N, y_type, y);
   return hipGetLastError();
 }
 

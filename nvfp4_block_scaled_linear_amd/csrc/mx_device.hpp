@@ -47,4 +47,84 @@ __device__ __forceinline__ uint32_t f32_to_bf16_any(float v) {
   return v != v ? 0x7FC0u : f32_to_bf16_rne(v);
 }
 
+// two f32 -> BF16 pair, round to nearest even, NaN stays NaN
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// largest magnitude (f32 bits) of n BF16 pairs
+template <int n>
+__device__ __forceinline__ uint32_t amax_pairs(const uint32_t* h) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < n; i++) {
+    const uint32_t lo = (h[i] & 0x7FFFu) << 16, hi = h[i] & 0x7FFF0000u;
+    m = m > lo ? m : lo;
+    m = m > hi ? m : hi;
+  }
+  return m;
+}
+
+// two BF16 pairs -> their four codes (16 bits) at scale byte s
+__device__ __forceinline__ uint32_t codes_of_pairs(uint32_t a, uint32_t b, uint32_t s) {
+  const int up = 127 - (int)s;
+  const float q0 = __builtin_ldexpf(__uint_as_float(a << 16), up);
+  const float q1 = __builtin_ldexpf(__uint_as_float(a & 0xFFFF0000u), up);
+  const float q2 = __builtin_ldexpf(__uint_as_float(b << 16), up);
+  const float q3 = __builtin_ldexpf(__uint_as_float(b & 0xFFFF0000u), up);
+  return e2m1_rne2<1>(e2m1_rne2<0>(0u, q0, q1), q2, q3);
+}
+
+// ---------------------------------------------------------------------------------------
+// Loads from memory straight into LDS, through a buffer descriptor: lanes out of its range
+// write zeros and touch no memory. They are instructions without outputs, so the compiler
+// neither tracks nor waits for them: a counted wait (wait_loads) stands before the reads.
+// ---------------------------------------------------------------------------------------
+constexpr uint32_t kOutOfRange = 0x80000000u;  // an offset past every descriptor's range
+
+__device__ __forceinline__ u32x4 lds_load_rsrc(const void* base, int64_t bytes) {
+  const uint64_t p = (uint64_t)(uintptr_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32) & 0xFFFFu);
+  const uint32_t n = __builtin_amdgcn_readfirstlane((uint32_t)(bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes));
+  return u32x4{lo, hi, n, 0x00020000u};
+}
+
+// BYTES (16, 4 or 1) bytes per lane from offset `off`; lane l's go to lds + l * max(BYTES, 4)
+// (a byte as a dword). lds is the same in all lanes.
+template <int BYTES>
+__device__ __forceinline__ void lds_load(u32x4 rsrc, uint32_t off, uint32_t lds) {
+  static_assert(BYTES == 16 || BYTES == 4 || BYTES == 1, "");
+  if (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+  else if (BYTES == 4)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_ubyte %0, %1, 0 offen lds"
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+}
+
+// all but this wave's latest N loads are done, and its LDS reads
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// this wave's LDS reads are done (what they read may be overwritten)
+__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// all but the latest N loads and the LDS reads are done, and the workgroup's other waves have come as far
+template <int N>
+__device__ __forceinline__ void wait_loads_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_address(void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)p;
+}
+
 }  // namespace nvfp4

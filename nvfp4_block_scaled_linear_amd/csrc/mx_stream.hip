@@ -1,58 +1,182 @@
 // MXFP4 products for few activation rows: the weight is streamed once for all of them.
 //
-// Decode-sized products are bound by the weight's bytes, and a launch that lasts a few
-// microseconds by how soon all its loads are in flight. So a workgroup takes 16 * NT weight
-// rows (SwiGLU: gate rows and the up rows that belong to them) and its W waves split K into
-// runs of 128-k steps; a wave keeps a ring of U steps of loads in registers, and the waves'
-// partial sums meet in LDS and are added in wave order, so results do not depend on timing.
+// Decode-sized products are bound by the weight's bytes, and a launch of a few microseconds by
+// how soon its loads are in flight and how few cache lines they look up. A workgroup takes
+// 16 * NT weight rows (SwiGLU: gate rows and the up rows that belong to them); its W waves
+// split K into runs of 128-k steps, each through an LDS ring of its own that holds U steps of
+// both operands, so no wave waits for another before the end, when their partial sums are
+// added in wave order (results do not depend on timing).
 //
-// A step of a 16-row tile is one 16-byte load of codes per lane: lane l = c + 16g holds block
-// g (32 k) of row c, so that a row's 64 bytes are read by neighbouring lanes.
-//  - MXFP4 activations: the activation rows are loaded alike and one scaled MFMA does the step.
-//  - BF16 activations: MFMA j covers block j, lane (c, g) holding k = 8g + [0, 8) of it, so that
-//    the activations' loads run along their rows (64 bytes of a row per instruction); the
-//    codes are brought into that order by a 4 x 4 transpose of dwords between the lanes of a
-//    row, four lane swaps a step.
-// Loads are buffer loads, out of range (zeros, no memory touched) past the rows, past K and
-// past a wave's run, so no branch stands around them.
+// The MFMA wants 16 consecutive lanes on 16 different rows. Loaded into registers like that, a
+// load looks up a cache line per lane; loads into LDS (lds_load) take the rows as they lie,
+// four lanes to a row's 64 bytes of codes, 16 lanes to its 256 bytes of BF16, and the LDS reads
+// bring the operands into order. Row r's 16-byte piece q lies at slot q ^ f(r), so that the 16
+// rows that lanes read together fall into different banks.
+//  - MXFP4 activations: one scaled MFMA over the step per 16 weight rows.
+//  - BF16 activations: lane (c, g) = c + 16g decodes the 32 codes of block g of its row with the
+//    block's scale, and MFMA j is over k = 32g + 8j + [0, 8).
+// Loads past the rows, past K and past a wave's run are out of range: every step issues the
+// same number, which is what the counted waits go by.
 #include "mx_device.hpp"
 #include "mx_kernels.hpp"
+#include "mx_routes.hpp"
 
 namespace nvfp4 {
 namespace {
 
-constexpr uint32_t kOOB = 0x80000000u;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
-                                           (int)(bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes), 0x00020000);
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 v = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, v);
-}
-
-// scale bytes of a step and row: one dword when DW (K % 128 == 0 and dword-aligned scales),
-// otherwise one byte load per block that the lane needs
-template <int ACT, int TM, int NT>
-struct Step {
-  u32x4 w[NT], x[TM][ACT == MXFP4_ACT_BF16 ? 4 : 1];
-  uint32_t ws[NT], xs[TM];
-};
-
-template <int ACT_, int TM_, int NT_, int W_, int U_, bool DW_>
+// XR activation rows (4, or TM tiles of 16), NT tiles of 16 weight rows, W waves, U steps in
+// the ring; DW: a row's four scale bytes of a step are loaded as one dword (K % 128 == 0 and
+// dword-aligned scales), otherwise a byte per lane
+template <int ACT_, int XR_, int NT_, int W_, int U_, bool DW_>
 struct Cfg {
-  static constexpr int ACT = ACT_, TM = TM_, NT = NT_, W = W_, U = U_;
+  static constexpr int ACT = ACT_, XR = XR_, TM = (XR_ + 15) / 16, NT = NT_, W = W_, U = U_;
   static constexpr bool DW = DW_, MX = ACT_ == MXFP4_ACT_MXFP4;
+  static constexpr int XMAX = MX ? TM : XR / 4;  // 1 KiB loads of activations a step
+  static constexpr int SW = DW ? 1 : NT, SX = MX ? (DW ? 1 : TM) : 0;  // loads of scales
+  static constexpr int W0 = 0, X0 = 1024 * NT, S0 = X0 + 1024 * XMAX, STEP = S0 + 256 * (SW + SX);
+  static constexpr int RING = STEP * U;                // of a wave
+  static constexpr int PART = 1024 * NT * TM;          // partial sums of a wave
+  static constexpr int LDS = W * (RING > PART ? RING : PART);
+  static_assert(NT <= 4 && TM <= 4 && LDS <= 160 * 1024, "");
 };
 
-template <class C, bool GROUPED, int SWIGLU>
+struct Operands {
+  u32x4 w, ws, x, xs;  // descriptors
+};
+
+// One wave's run [s0, s1) of K steps over the rows whose lanes' offsets are xo / xso.
+template <class C>
+__device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, const uint8_t* ring_p,
+                                          int s0, int s1, int nb, const uint32_t* wo,
+                                          const uint32_t* wso, const uint32_t* xo,
+                                          const uint32_t* xso, f32x4 (&acc)[C::NT][C::TM]) {
+  constexpr int XI = C::XMAX, LOADS = C::NT + XI + C::SW + C::SX;
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  // this lane's block of a load of codes, and its 16-byte piece of a load of BF16 rows
+  const int wq = (lane & 3) ^ ((lane >> 4) & 3);
+  const auto issue = [&](int s, int u) {
+    const uint32_t base = ring + u * C::STEP;
+    const bool in = s < s1;
+    const uint32_t w_at = in && 4 * s + wq < nb ? 64 * s : kOutOfRange;
+#pragma unroll
+    for (int t = 0; t < C::NT; t++)
+      lds_load<16>(d.w, w_at == kOutOfRange ? kOutOfRange : wo[t] + w_at, base + C::W0 + 1024 * t);
+#pragma unroll
+    for (int i = 0; i < XI; i++) {
+      uint32_t off;
+      if (C::MX) {
+        off = w_at == kOutOfRange ? kOutOfRange : xo[i] + w_at;
+      } else {
+        const int q = (lane & 15) ^ ((4 * i + (lane >> 4)) & 15);  // of the row's 16 pieces
+        off = in && 4 * s + (q >> 2) < nb ? xo[i] + 256 * s : kOutOfRange;
+      }
+      lds_load<16>(d.x, off, base + C::X0 + 1024 * i);
+    }
+    if (C::DW) {
+      lds_load<4>(d.ws, in ? wso[0] + 4 * s : kOutOfRange, base + C::S0);
+      if (C::MX) lds_load<4>(d.xs, in ? xso[0] + 4 * s : kOutOfRange, base + C::S0 + 256);
+    } else {
+      const bool sin = in && 4 * s + (lane & 3) < nb;
+#pragma unroll
+      for (int t = 0; t < C::NT; t++)
+        lds_load<1>(d.ws, sin ? wso[t] + 4 * s : kOutOfRange, base + C::S0 + 256 * t);
+#pragma unroll
+      for (int x = 0; x < C::SX; x++)
+        lds_load<1>(d.xs, sin ? xso[x] + 4 * s : kOutOfRange, base + C::S0 + 256 * (C::SW + x));
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < C::U - 1; u++) issue(s0 + u, u);
+  int u = 0;
+  for (int s = s0; s < s1; s++) {
+    wait_lds_reads();  // of the step whose bytes the next loads overwrite
+    issue(s + C::U - 1, u == 0 ? C::U - 1 : u - 1);
+    wait_loads<(C::U - 1) * LOADS>();
+    const uint8_t* b = ring_p + u * C::STEP;
+    // scale byte of block g of row `row` (of the weight, or behind SW loads of the activations)
+    const auto scale = [&](int side, int row) -> uint32_t {
+      const uint8_t* p = b + C::S0 + 256 * side;
+      return C::DW ? p[4 * row + g] : p[16 * row + 4 * g];
+    };
+    if (C::MX) {
+      u32x4 xf[C::TM];
+      uint32_t xs[C::TM];
+#pragma unroll
+      for (int x = 0; x < C::TM; x++) {
+        xf[x] = *reinterpret_cast<const u32x4*>(b + C::X0 + 1024 * x + 64 * c + ((g ^ (c >> 2)) << 4));
+        xs[x] = scale(C::SW, 16 * x + c);
+      }
+#pragma unroll
+      for (int t = 0; t < C::NT; t++) {
+        const u32x4 wf = *reinterpret_cast<const u32x4*>(b + C::W0 + 1024 * t + 64 * c + ((g ^ (c >> 2)) << 4));
+        const uint32_t ws = scale(0, 16 * t + c);
+#pragma unroll
+        for (int x = 0; x < C::TM; x++) acc[t][x] = mfma_mx(wf, xf[x], acc[t][x], ws, xs[x]);
+      }
+    } else {
+      u32x4 xf[C::TM][4];
+#pragma unroll
+      for (int x = 0; x < C::TM; x++) {
+        // rows past the loaded ones read others' values, into columns that nobody stores
+        const int r = (16 * x + c) % (4 * XI);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          xf[x][j] = *reinterpret_cast<const u32x4*>(b + C::X0 + 256 * r + (((4 * g + j) ^ (r & 15)) << 4));
+      }
+#pragma unroll
+      for (int t = 0; t < C::NT; t++) {
+        const u32x4 wf = *reinterpret_cast<const u32x4*>(b + C::W0 + 1024 * t + 64 * c + ((g ^ (c >> 2)) << 4));
+        const float ws = e8m0_operand(scale(0, 16 * t + c));
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const u32x4 w = mx_decode8(wf[j], ws);
+#pragma unroll
+          for (int x = 0; x < C::TM; x++) acc[t][x] = mfma16(w, xf[x][j], acc[t][x]);
+        }
+      }
+    }
+    u = u + 1 == C::U ? 0 : u + 1;
+  }
+  wait_loads<0>();
+}
+
+// How a grouped workgroup finds its expert and the routes of it
+enum Mode {
+  kDense,
+  kByExpert,  // few routes in all: the workgroup takes an expert and looks for it in topk_ids
+  kBySlot     // from the grouping: a slot record's first kMxSlotRoutes routes, or a list tile
+};
+constexpr int kScanRoutes = 256;  // kByExpert: routes in all, four per lane
+
+// bits of the routes 64 * i + lane that expert e keeps: those that hold e and are not a repeat
+// of it within their token (top_k <= 64: the token starts in this group of 64 or the last)
+__device__ __forceinline__ void scan_routes(const int32_t* ids, int R, int top_k, int e,
+                                            uint64_t (&kept)[kScanRoutes / 64]) {
+  const int lane = threadIdx.x & 63;
+  int32_t id[kScanRoutes / 64];
+#pragma unroll
+  for (int i = 0; i < kScanRoutes / 64; i++) id[i] = 64 * i + lane < R ? ids[64 * i + lane] : -1;
+  uint64_t last = 0u;
+#pragma unroll
+  for (int i = 0; i < kScanRoutes / 64; i++) {
+    const uint64_t m = __ballot(id[i] == e);
+    const int before = (64 * i + lane) % top_k;  // routes of the token before this one
+    // bit 63: the route before this one, bit 62 the one before that, ...
+    const uint64_t window = (lane ? m << (64 - lane) : 0u) | last >> lane;
+    const bool repeat = before && (window >> (64 - before)) != 0u;
+    kept[i] = __ballot(id[i] == e && !repeat);
+    last = m;
+  }
+}
+
+template <class C, int MODE, int SWIGLU>
 __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
+  constexpr bool GROUPED = MODE != kDense;
   constexpr int NO = SWIGLU ? C::NT / 2 : C::NT;  // 16-column tiles of output
   static_assert(SWIGLU != MXFP4_OUT_SWIGLU_MXFP4 || NO % 2 == 0, "whole blocks of 32 columns");
-  extern __shared__ __attribute__((aligned(16))) f32x4 part[];  // [W][NT][TM][64]
+  static_assert(!GROUPED || C::TM == 1, "a grouped pass has at most 16 rows");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  __shared__ int32_t route_list[C::W][16];  // the pass's routes, a copy for each wave
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t N = a.N, K = a.K, half = N >> 1;
@@ -60,160 +184,141 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
   const int nb = (int)(K >> 5);
   const int64_t nbn = (cols + 16 * NO - 1) / (16 * NO);
   const int64_t n0 = (blockIdx.x % nbn) * (16 * NO);
+  const int group = (int)(blockIdx.x / nbn);
   const uint8_t* wc = a.w_codes;
   const uint8_t* wsc = a.w_scales;
-  int beg = 0, end = (int)a.M;
-  const int32_t* rec = nullptr;
-  if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4) {
-    // scales of dropped routes, shared out over the launch (the grouping clears their codes)
-    const int64_t bytes = N >> 6;
-    for (int64_t r = (int64_t)blockIdx.x * blockDim.x + tid; r < a.R; r += (int64_t)gridDim.x * blockDim.x)
-      if (a.route_expert[r] < 0)
-        for (int64_t b = 0; b < bytes; b++) a.y_scales[r * bytes + b] = 0;
+  int count = (int)a.M, first = 0, e = 0;  // rows; bySlot: their place in `sorted`
+  int32_t my_route = 0;                    // bySlot: routes of the first pass
+  uint64_t kept[kScanRoutes / 64];
+  if (MODE == kByExpert) {
+    e = group;
+    if (blockIdx.x == 0) drop_routes<SWIGLU>(a);
+    scan_routes(a.ids, (int)a.R, a.top_k, e, kept);
+    count = 0;
+#pragma unroll
+    for (int i = 0; i < kScanRoutes / 64; i++) count += __builtin_popcountll(kept[i]);
+    if (count == 0) return;
+  }
+  if (MODE == kBySlot) {
+    if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4) clear_dropped_scales(a);
+    if (group < a.max_slots) {
+      const int32_t v = lane < kSlotInts ? a.slots[(int64_t)kSlotInts * group + lane] : 0;
+      e = __builtin_amdgcn_readlane(v, 0);
+      if (e < 0) return;
+      first = __builtin_amdgcn_readlane(v, 1);
+      count = __builtin_amdgcn_readlane(v, 2) - first;
+      count = count < kMxSlotRoutes ? count : kMxSlotRoutes;
+      const int n = __builtin_amdgcn_readlane(v, 3);
+      my_route = __shfl(v, 4 + c, 64);
+      if (n < count && c >= n && c < count) my_route = a.sorted[first + c];
+    } else {
+      const int tile = group - a.max_slots;
+      if (tile >= *a.n_tiles) return;
+      e = a.tiles[2 * tile];
+      first = a.tiles[2 * tile + 1];
+      count = a.offsets[e + 1] - first;
+      count = count < kMxSlotRoutes ? count : kMxSlotRoutes;
+      my_route = c < count ? a.sorted[first + c] : 0;
+    }
   }
   if (GROUPED) {
-    rec = a.slots + kSlotInts * (blockIdx.x / nbn);
-    const int e = rec[0];
-    if (e < 0) return;
-    beg = rec[1];
-    end = rec[2];
     wc += (int64_t)e * N * (K >> 1);
     wsc += (int64_t)e * N * nb;
   }
-  // weight rows of this lane, from the tile's first row (SwiGLU: from the weight's)
-  const int64_t r0 = SWIGLU ? 0 : n0;
-  const auto wr = rsrc_of(wc + r0 * (K >> 1), (N - r0) * (K >> 1));
-  const auto wsr = rsrc_of(wsc + r0 * nb, (N - r0) * nb);
-  uint32_t wo[C::NT], wso[C::NT];
+  Operands d;
+  const int64_t r0 = SWIGLU ? 0 : n0;  // weight row that the offsets count from
+  d.w = lds_load_rsrc(wc + r0 * (K >> 1), (N - r0) * (K >> 1));
+  d.ws = lds_load_rsrc(wsc + r0 * nb, (N - r0) * nb);
+  const int64_t xpitch = C::MX ? K >> 1 : a.ldx * 2;
+  d.x = lds_load_rsrc(a.x, (a.x_rows - 1) * xpitch + (C::MX ? K >> 1 : 2 * K));
+  d.xs = C::MX ? lds_load_rsrc(a.x_scales, a.x_rows * nb) : d.x;
+  // row i of weight tile t, from r0, or -1
+  const auto w_row = [&](int t, int i) -> int64_t {
+    const int64_t n = n0 + 16 * (t % NO) + i;
+    return n < cols ? n - r0 + (t >= NO ? half : 0) : -1;
+  };
+  const int wq = (lane & 3) ^ ((lane >> 4) & 3);
+  uint32_t wo[C::NT], wso[C::SW];
 #pragma unroll
   for (int t = 0; t < C::NT; t++) {
-    const int64_t n = n0 + 16 * (t % NO) + c;
-    const int64_t row = n - r0 + (t >= NO ? half : 0);
-    wo[t] = n < cols ? (uint32_t)(row * (K >> 1)) + 16 * g : kOOB;
-    wso[t] = n < cols ? (uint32_t)(row * nb) : kOOB;
+    const int64_t row = w_row(t, lane >> 2);
+    wo[t] = row >= 0 ? (uint32_t)(row * (K >> 1)) + 16 * wq : kOutOfRange;
+    if (!C::DW) wso[t] = row >= 0 ? (uint32_t)(row * nb) + (lane & 3) : kOutOfRange;
   }
-  // this wave's steps, a run of an even number (two steps are one 128-byte line of codes)
+  if (C::DW) {
+    const int64_t row = (lane >> 4) < C::NT ? w_row(lane >> 4, c) : -1;
+    wso[0] = row >= 0 ? (uint32_t)(row * nb) : kOutOfRange;
+  }
+  // this wave's steps: a run of an even number (two steps are one 128-byte line of codes)
   const int steps = (nb + 3) >> 2;
   const int per = ((steps + 2 * C::W - 1) / (2 * C::W)) * 2;
   const int s0 = wave * per, s1 = s0 + per < steps ? s0 + per : steps;
-  const int64_t xpitch = C::MX ? K >> 1 : a.ldx * 2;
-  const auto xr = rsrc_of(a.x, (a.x_rows - 1) * xpitch + (C::MX ? K >> 1 : 2 * K));
-  const auto xsr = C::MX ? rsrc_of(a.x_scales, a.x_rows * nb) : xr;
+  constexpr int WAVE = C::LDS / C::W;
+  const uint8_t* ring_p = smem + wave * WAVE;
+  const uint32_t ring = lds_address(smem) + wave * WAVE;
 
-  for (int p0 = beg; p0 < end; p0 += 16 * C::TM) {
-    uint32_t xo[C::TM], xso[C::TM];
-#pragma unroll
-    for (int x = 0; x < C::TM; x++) {
-      const int p = p0 + 16 * x + c;
-      int64_t row = p;
-      if (GROUPED && p < end) {
-        const int32_t route = p - beg < rec[3] ? rec[4 + p - beg] : a.sorted[p];
-        row = a.rows_per_token ? route / a.top_k : route;
-      }
-      xo[x] = p < end ? (uint32_t)(row * xpitch) + 16 * g : kOOB;
-      xso[x] = p < end ? (uint32_t)(row * nb) : kOOB;
+  for (int p0 = 0; p0 < count; p0 += C::XR) {
+    const int rows = count - p0 < C::XR ? count - p0 : C::XR;
+    int32_t* const list = route_list[wave];
+    if (MODE == kBySlot) {
+      if (lane < 16 && lane >= p0 && lane - p0 < rows) list[lane - p0] = my_route;
     }
-    const auto load = [&](Step<C::ACT, C::TM, C::NT>& b, int s) {
-      const bool in = s < s1;
-      const bool mine = in && 4 * s + g < nb;  // this lane's block of codes
+    if (MODE == kByExpert) {
+      int before = 0;
 #pragma unroll
-      for (int t = 0; t < C::NT; t++) {
-        b.w[t] = __builtin_amdgcn_raw_buffer_load_b128(wr, mine ? wo[t] + 64 * s : kOOB, 0, 0);
-        if (C::DW) {
-          b.ws[t] = __builtin_amdgcn_raw_buffer_load_b32(wsr, in ? wso[t] + 4 * s : kOOB, 0, 0);
-        } else if (C::MX) {
-          b.ws[t] = __builtin_amdgcn_raw_buffer_load_b8(wsr, mine ? wso[t] + 4 * s + g : kOOB, 0, 0);
-        } else {
-          uint32_t v = 0u;
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-            v |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-                     wsr, in && 4 * s + j < nb ? wso[t] + 4 * s + j : kOOB, 0, 0) << (8 * j);
-          b.ws[t] = v;
-        }
+      for (int i = 0; i < kScanRoutes / 64; i++) {
+        const int at = before + __builtin_popcountll(kept[i] & ((1ull << lane) - 1)) - p0;
+        if ((kept[i] >> lane & 1) && at >= 0 && at < rows) list[at] = 64 * i + lane;
+        before += __builtin_popcountll(kept[i]);
       }
-#pragma unroll
-      for (int x = 0; x < C::TM; x++) {
-        if (C::MX) {
-          b.x[x][0] = __builtin_amdgcn_raw_buffer_load_b128(xr, mine ? xo[x] + 64 * s : kOOB, 0, 0);
-          if (C::DW)
-            b.xs[x] = __builtin_amdgcn_raw_buffer_load_b32(xsr, in ? xso[x] + 4 * s : kOOB, 0, 0);
-          else
-            b.xs[x] = __builtin_amdgcn_raw_buffer_load_b8(xsr, mine ? xso[x] + 4 * s + g : kOOB, 0, 0);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-            b.x[x][j] = __builtin_amdgcn_raw_buffer_load_b128(
-                xr, in && 4 * s + j < nb ? xo[x] + 256 * s + 64 * j : kOOB, 0, 0);
-        }
-      }
+    }
+    if (GROUPED) __builtin_amdgcn_wave_barrier();
+    // output row of the pass's i-th row, and its x row or -1
+    const auto y_row = [&](int i) -> int64_t { return GROUPED ? list[i] : p0 + i; };
+    const auto x_row = [&](int i) -> int64_t {
+      if (i >= rows) return -1;
+      const int64_t r = y_row(i);
+      return GROUPED && a.rows_per_token ? r / a.top_k : r;
     };
-
+    uint32_t xo[C::XMAX], xso[C::SX > 0 ? C::SX : 1];
+#pragma unroll
+    for (int i = 0; i < C::XMAX; i++) {
+      const int64_t row = x_row(C::MX ? 16 * i + (lane >> 2) : 4 * i + (lane >> 4));
+      const int q = C::MX ? wq : (lane & 15) ^ ((4 * i + (lane >> 4)) & 15);
+      xo[i] = row >= 0 ? (uint32_t)(row * xpitch) + 16 * q : kOutOfRange;
+      if (C::MX && !C::DW) xso[i] = row >= 0 ? (uint32_t)(row * nb) + (lane & 3) : kOutOfRange;
+    }
+    if (C::MX && C::DW) {
+      const int64_t row = (lane >> 4) < C::TM ? x_row(lane) : -1;
+      xso[0] = row >= 0 ? (uint32_t)(row * nb) : kOutOfRange;
+    }
     f32x4 acc[C::NT][C::TM];
 #pragma unroll
     for (int t = 0; t < C::NT; t++)
 #pragma unroll
       for (int x = 0; x < C::TM; x++) acc[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const auto compute = [&](Step<C::ACT, C::TM, C::NT>& b) {
-      if (C::MX) {
-        const int sh = C::DW ? 8 * g : 0;
-#pragma unroll
-        for (int t = 0; t < C::NT; t++)
-#pragma unroll
-          for (int x = 0; x < C::TM; x++)
-            acc[t][x] = mfma_mx(b.w[t], b.x[x][0], acc[t][x], b.ws[t] >> sh, b.xs[x] >> sh);
-      } else {
-#pragma unroll
-        for (int t = 0; t < C::NT; t++) {
-          transpose4(b.w[t]);
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const u32x4 w = mx_decode8(b.w[t][j], e8m0_operand((b.ws[t] >> (8 * j)) & 0xFFu));
-#pragma unroll
-            for (int x = 0; x < C::TM; x++) acc[t][x] = mfma16(w, b.x[x][j], acc[t][x]);
-          }
-        }
-      }
-    };
-
-    if (s0 < s1) {
-      Step<C::ACT, C::TM, C::NT> ring[C::U];
-#pragma unroll
-      for (int u = 0; u < C::U; u++) load(ring[u], s0 + u);
-      int s = s0;
-      for (; s + C::U < s1; s += C::U) {
-#pragma unroll
-        for (int u = 0; u < C::U; u++) {
-          compute(ring[u]);
-          load(ring[u], s + C::U + u);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < C::U; u++) compute(ring[u]);
-    }
-
-    if (GROUPED && p0 != beg) __syncthreads();  // the last pass's partial sums have been read
+    if (s0 < s1) run_steps<C>(d, ring, ring_p, s0, s1, nb, wo, wso, xo, xso, acc);
+    // partial sums of this wave [NT][TM][64], in the bytes of its ring
+    const auto part = [&](int w) { return reinterpret_cast<f32x4*>(smem + w * WAVE); };
 #pragma unroll
     for (int t = 0; t < C::NT; t++)
 #pragma unroll
-      for (int x = 0; x < C::TM; x++) part[((wave * C::NT + t) * C::TM + x) * 64 + lane] = acc[t][x];
+      for (int x = 0; x < C::TM; x++) part(wave)[(t * C::TM + x) * 64 + lane] = acc[t][x];
     __syncthreads();
-    const auto total = [&](int t, int x, int l) {
-      f32x4 v = part[(t * C::TM + x) * 64 + l];
+    const auto total = [&](int t, int x) {
+      f32x4 v = part(0)[(t * C::TM + x) * 64 + lane];
 #pragma unroll
-      for (int w = 1; w < C::W; w++) v += part[((w * C::NT + t) * C::TM + x) * 64 + l];
+      for (int w = 1; w < C::W; w++) v += part(w)[(t * C::TM + x) * 64 + lane];
       return v;
     };
     // an item: four columns per lane of a 16 x 16 tile (MXFP4: of two, which make a block)
     constexpr int TS = SWIGLU == MXFP4_OUT_SWIGLU_MXFP4 ? 2 : 1;
     for (int i = wave; i < NO / TS * C::TM; i += C::W) {
       const int t = i % (NO / TS) * TS, x = i / (NO / TS);
-      const int p = p0 + 16 * x + c;
-      const bool ok = p < end;
-      int64_t row = p;
-      if (GROUPED) row = !ok ? 0 : p - beg < rec[3] ? rec[4 + p - beg] : a.sorted[p];
+      const bool ok = 16 * x + c < rows;
+      const int64_t row = ok ? y_row(16 * x + c) : 0;
       const int64_t n = n0 + 16 * t + 4 * g;
-      const f32x4 v = total(t, x, lane);
+      const f32x4 v = total(t, x);
       if (!SWIGLU) {
         if (!ok) continue;
 #pragma unroll
@@ -226,9 +331,13 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
         }
         continue;
       }
-      const f32x4 u = total(NO + t, x, lane);
-      const uint32_t h[2] = {bf16_pair(silu(v[0]) * u[0], silu(v[1]) * u[1]),
-                             bf16_pair(silu(v[2]) * u[2], silu(v[3]) * u[3])};
+      uint32_t h[2 * TS];
+#pragma unroll
+      for (int k = 0; k < TS; k++) {
+        const f32x4 gt = k ? total(t + k, x) : v, u = total(NO + t + k, x);
+        h[2 * k] = bf16_pair(silu(gt[0]) * u[0], silu(gt[1]) * u[1]);
+        h[2 * k + 1] = bf16_pair(silu(gt[2]) * u[2], silu(gt[3]) * u[3]);
+      }
       if (SWIGLU == MXFP4_OUT_SWIGLU_BF16) {
 #pragma unroll
         for (int q = 0; q < 4; q++)
@@ -236,16 +345,7 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
             static_cast<uint16_t*>(a.y)[row * half + n + q] = (uint16_t)(h[q >> 1] >> (16 * (q & 1)));
         continue;
       }
-      const f32x4 v1 = total(t + 1, x, lane), u1 = total(NO + t + 1, x, lane);
-      const uint32_t k[4] = {h[0], h[1], bf16_pair(silu(v1[0]) * u1[0], silu(v1[1]) * u1[1]),
-                             bf16_pair(silu(v1[2]) * u1[2], silu(v1[3]) * u1[3])};
-      uint32_t amax = 0u;
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const uint32_t lo = (k[q] & 0x7FFFu) << 16, hi = k[q] & 0x7FFF0000u;
-        amax = amax > lo ? amax : lo;
-        amax = amax > hi ? amax : hi;
-      }
+      uint32_t amax = amax_pairs<2 * TS>(h);
       uint32_t o = __shfl_xor(amax, 16, 64);
       amax = amax > o ? amax : o;
       o = __shfl_xor(amax, 32, 64);
@@ -254,71 +354,64 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
       const bool bad = amax >= 0x7F800000u;
       if (!ok || n >= half) continue;  // blocks end where the columns do
 #pragma unroll
-      for (int q = 0; q < 2; q++) {
-        float f[4];
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-          f[2 * j] = __builtin_ldexpf(__uint_as_float(k[2 * q + j] << 16), 127 - (int)sc);
-          f[2 * j + 1] = __builtin_ldexpf(__uint_as_float(k[2 * q + j] & 0xFFFF0000u), 127 - (int)sc);
-        }
-        const uint32_t code = e2m1_rne2<1>(e2m1_rne2<0>(0u, f[0], f[1]), f[2], f[3]);
-        *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.y) + row * (half >> 1) + ((n + 16 * q) >> 1)) =
-            bad ? 0 : (uint16_t)code;
-      }
+      for (int k = 0; k < TS; k++)
+        *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.y) + row * (half >> 1) + ((n + 16 * k) >> 1)) =
+            bad ? 0 : (uint16_t)codes_of_pairs(h[2 * k], h[2 * k + 1], sc);
       if (g == 0) a.y_scales[row * (half >> 5) + (n >> 5)] = (uint8_t)(bad ? kE8M0Nan : sc);
     }
-    if (!GROUPED) return;  // dense: M <= 16 * TM
+    if (!GROUPED) return;  // dense: M <= XR
+    __syncthreads();       // the partial sums have been read
   }
 }
 
-template <class C>
-hipError_t launch_cfg(const MxArgs& a, int64_t max_slots, hipStream_t stream) {
+template <class C, int MODE>
+hipError_t launch_mode(const MxArgs& a, int64_t groups, hipStream_t stream) {
   const int64_t no = a.swiglu ? C::NT / 2 : C::NT;
   const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
-  const int64_t groups = (cols + 16 * no - 1) / (16 * no) * (a.slots ? max_slots : 1);
-  if (groups * 64 * C::W > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
-  const size_t lds = sizeof(f32x4) * 64 * C::W * C::NT * C::TM;
-  auto k = !a.slots ? mx_stream<C, false, 0> : mx_stream<C, true, 0>;
-  if constexpr (C::NT == 4) {
-    if (a.swiglu)
-      k = a.swiglu == MXFP4_OUT_SWIGLU_BF16 ? mx_stream<C, true, MXFP4_OUT_SWIGLU_BF16>
-                                            : mx_stream<C, true, MXFP4_OUT_SWIGLU_MXFP4>;
+  const int64_t blocks = (cols + 16 * no - 1) / (16 * no) * groups;
+  if (blocks * 64 * C::W > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
+  auto k = mx_stream<C, MODE, 0>;
+  if constexpr (MODE != kDense && C::NT % 4 == 0) {
+    if (a.swiglu == MXFP4_OUT_SWIGLU_BF16) k = mx_stream<C, MODE, MXFP4_OUT_SWIGLU_BF16>;
+    if (a.swiglu == MXFP4_OUT_SWIGLU_MXFP4) k = mx_stream<C, MODE, MXFP4_OUT_SWIGLU_MXFP4>;
   }
-  hipLaunchKernelGGL(k, dim3((uint32_t)groups), dim3(64 * C::W), lds, stream, a);
+  hipLaunchKernelGGL(k, dim3((uint32_t)blocks), dim3(64 * C::W), C::LDS, stream, a);
   return hipGetLastError();
 }
 
-template <int ACT, int TM, int NT, int U>
-hipError_t launch_rows(const MxArgs& a, bool dw, int64_t max_slots, hipStream_t stream) {
-  if (a.K >= 2048) {
-    return dw ? launch_cfg<Cfg<ACT, TM, NT, 8, U, true>>(a, max_slots, stream)
-              : launch_cfg<Cfg<ACT, TM, NT, 8, U, false>>(a, max_slots, stream);
+template <class C>
+hipError_t launch_cfg(const MxArgs& a, hipStream_t stream) {
+  if constexpr (C::TM == 1) {
+    if (a.ids) return launch_mode<C, kByExpert>(a, a.num_experts, stream);
+    if (a.slots) return launch_mode<C, kBySlot>(a, a.max_slots + a.max_tiles, stream);
   }
-  return dw ? launch_cfg<Cfg<ACT, TM, NT, 4, U, true>>(a, max_slots, stream)
-            : launch_cfg<Cfg<ACT, TM, NT, 4, U, false>>(a, max_slots, stream);
+  return launch_mode<C, kDense>(a, 1, stream);
+}
+
+//LAUNCH
+template <int ACT, int XR, int NT, int W, int U>
+hipError_t launch_rows(const MxArgs& a, hipStream_t stream) {
+  const bool dw = a.K % 128 == 0 && ((uintptr_t)a.w_scales | (uintptr_t)a.x_scales) % 4 == 0;
+  return dw ? launch_cfg<Cfg<ACT, XR, NT, W, U, true>>(a, stream)
+            : launch_cfg<Cfg<ACT, XR, NT, W, U, false>>(a, stream);
 }
 
 template <int ACT>
-hipError_t launch_act(const MxArgs& a, int64_t rows, int64_t max_slots, hipStream_t stream) {
-  const bool dw = a.K % 128 == 0 && ((uintptr_t)a.w_scales | (uintptr_t)a.x_scales) % 4 == 0;
-  if (a.swiglu) return launch_rows<ACT, 1, 4, 2>(a, dw, max_slots, stream);
-  if (rows <= 16) return launch_rows<ACT, 1, 2, 4>(a, dw, max_slots, stream);
-  if (rows <= 32) return launch_rows<ACT, 2, 2, 2>(a, dw, max_slots, stream);
-  return launch_rows<ACT, 4, 2, 2>(a, dw, max_slots, stream);
+hipError_t launch_act(const MxArgs& a, int64_t rows, hipStream_t stream) {
+  if (a.swiglu) return launch_rows<ACT, 16, 4, 4, 2>(a, stream);
+  if (rows <= 16) return launch_rows<ACT, 16, 2, 4, 2>(a, stream);
+  if (rows <= 32) return launch_rows<ACT, 32, 2, 4, 2>(a, stream);
+  return launch_rows<ACT, 64, 2, 4, 2>(a, stream);
 }
+//END
 
 }  // namespace
 
-bool mx_stream_takes(const MxArgs& a, int act_kind) {
-  // 32-bit offsets into the activations and one weight
-  const int64_t pitch = act_kind == MXFP4_ACT_MXFP4 ? a.K >> 1 : a.ldx * 2;
-  return a.x_rows * pitch < (int64_t)kOOB && a.N * (a.K >> 1) < (int64_t)kOOB;
-}
+int64_t mx_scan_routes() { return kScanRoutes; }
 
-hipError_t launch_mx_stream(const MxArgs& a, int act_kind, int64_t rows, int64_t max_slots,
-                            hipStream_t stream) {
-  return act_kind == MXFP4_ACT_BF16 ? launch_act<MXFP4_ACT_BF16>(a, rows, max_slots, stream)
-                                    : launch_act<MXFP4_ACT_MXFP4>(a, rows, max_slots, stream);
+hipError_t launch_mx_stream(const MxArgs& a, int act_kind, int64_t rows, hipStream_t stream) {
+  return act_kind == MXFP4_ACT_BF16 ? launch_act<MXFP4_ACT_BF16>(a, rows, stream)
+                                    : launch_act<MXFP4_ACT_MXFP4>(a, rows, stream);
 }
 
 }  // namespace nvfp4

@@ -19,46 +19,10 @@
 //    quantized.
 #include "mx_device.hpp"
 #include "mx_kernels.hpp"
+#include "mx_routes.hpp"
 
 namespace nvfp4 {
 namespace {
-
-constexpr uint32_t kOOB = 0x80000000u;
-
-__device__ __forceinline__ u32x4 make_rsrc(const void* base, int64_t bytes) {
-  const uint64_t p = (uint64_t)(uintptr_t)base;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32) & 0xFFFFu);
-  const uint32_t n = __builtin_amdgcn_readfirstlane((uint32_t)(bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes));
-  return u32x4{lo, hi, n, 0x00020000u};
-}
-
-// one load of BYTES bytes per lane into LDS: lane l's go to lds + l * max(BYTES, 4); lanes out
-// of the descriptor's range write zeros
-template <int BYTES>
-__device__ __forceinline__ void load_lds(u32x4 rsrc, uint32_t off, uint32_t lds) {
-  if (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
-  else if (BYTES == 4)
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_ubyte %0, %1, 0 offen lds"
-                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
-}
-
-// all but this wave's latest N loads are done, its LDS reads too, and the other waves are here
-template <int N>
-__device__ __forceinline__ void wait_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 v = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, v);
-}
 
 template <int ACT_, int BM_, int BN_, int WX_, int WW_, int D_, bool BYTE_SCALES_>
 struct Shape {
@@ -103,13 +67,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   int64_t mt, nt;
   {
     const int64_t nbm = GROUPED ? *a.n_tiles : (a.M + S::BM - 1) / S::BM;
-    if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4) {
-      // scales of dropped routes, shared out over the launch (the grouping clears their codes)
-      const int64_t bytes = N >> 6;
-      for (int64_t r = (int64_t)blockIdx.x * S::T + tid; r < a.R; r += (int64_t)gridDim.x * S::T)
-        if (a.route_expert[r] < 0)
-          for (int64_t b = 0; b < bytes; b++) a.y_scales[r * bytes + b] = 0;
-    }
+    if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4) clear_dropped_scales(a);
     const int64_t total = nbm * nbn;
     if (blockIdx.x >= total) return;
     const int64_t q = total / 8, r = total % 8, x = blockIdx.x % 8;
@@ -144,9 +102,9 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   };
   const int64_t xpitch = S::MX ? K >> 1 : a.ldx * 2;  // bytes
   const int64_t x_last = GROUPED ? a.x_rows : rows_m;
-  const u32x4 xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (GROUPED ? 0 : m0 * xpitch),
+  const u32x4 xr = lds_load_rsrc(static_cast<const uint8_t*>(a.x) + (GROUPED ? 0 : m0 * xpitch),
                              (x_last - 1) * xpitch + (S::MX ? K >> 1 : 2 * K));
-  const u32x4 wr = make_rsrc(wc + (SWIGLU ? 0 : n0 * (K >> 1)), (N - (SWIGLU ? 0 : n0)) * (K >> 1));
+  const u32x4 wr = lds_load_rsrc(wc + (SWIGLU ? 0 : n0 * (K >> 1)), (N - (SWIGLU ? 0 : n0)) * (K >> 1));
   // weight row of tile row t relative to that base, or -1
   const auto w_row = [&](int t) -> int64_t {
     if (!SWIGLU) return n0 + t < N ? t : -1;
@@ -163,7 +121,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     const int r = S::MX ? p >> 2 : p >> 3;
     const int q = S::MX ? (p & 3) ^ ((r >> 2) & 3) : (p & 7) ^ ((r >> 1) & 7);
     xk[i] = q;
-    xo[i] = r < rows_m ? (uint32_t)(x_row(r) * xpitch) + 16 * q : kOOB;
+    xo[i] = r < rows_m ? (uint32_t)(x_row(r) * xpitch) + 16 * q : kOutOfRange;
   }
 #pragma unroll
   for (int i = 0; i < S::NW; i++) {
@@ -179,10 +137,10 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     }
     wk[i] = q;
     const int64_t row = w_row(t);
-    wo[i] = row >= 0 ? (uint32_t)(row * (K >> 1)) + 16 * q : kOOB;
+    wo[i] = row >= 0 ? (uint32_t)(row * (K >> 1)) + 16 * q : kOutOfRange;
   }
-  const u32x4 wsr = make_rsrc(ws + (SWIGLU ? 0 : n0 * nb), (N - (SWIGLU ? 0 : n0)) * nb);
-  const u32x4 xsr = S::MX ? make_rsrc(a.x_scales + (GROUPED ? 0 : m0 * nb), x_last * nb) : wsr;
+  const u32x4 wsr = lds_load_rsrc(ws + (SWIGLU ? 0 : n0 * nb), (N - (SWIGLU ? 0 : n0)) * nb);
+  const u32x4 xsr = S::MX ? lds_load_rsrc(a.x_scales + (GROUPED ? 0 : m0 * nb), x_last * nb) : wsr;
   // scale loads: p-th of the stage. BF16: weight row p / 2, block p % 2. MXFP4: rows of the
   // weight, then of the activations, four blocks (one dword, or four byte loads) each. Whole
   // waves read one side (BN is a multiple of 64), so the descriptor is uniform.
@@ -197,10 +155,10 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     int64_t row = -1;
     if (t < S::BN) row = w_row(t);
     else if (S::MX && t - S::BN < rows_m) row = x_row(t - S::BN);
-    so[i] = row >= 0 ? (uint32_t)(row * nb) + sk[i] : kOOB;
+    so[i] = row >= 0 ? (uint32_t)(row * nb) + sk[i] : kOutOfRange;
   }
 
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  const uint32_t lds0 = lds_address(smem);
   const int nblk = (int)nb;
   const auto issue = [&](int st, int buf) {
     const uint32_t base = lds0 + buf * S::STAGE;
@@ -208,16 +166,16 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     for (int i = 0; i < S::NX; i++) {
       // a BF16 piece is in range when its block is: pieces 4 per block
       const int b = S::MX ? 4 * st + xk[i] : 2 * st + (xk[i] >> 2);
-      load_lds<16>(xr, b < nblk ? xo[i] + st * S::XB : kOOB, base + S::X0 + (i * S::T + wave * 64) * 16);
+      lds_load<16>(xr, b < nblk ? xo[i] + st * S::XB : kOutOfRange, base + S::X0 + (i * S::T + wave * 64) * 16);
     }
 #pragma unroll
     for (int i = 0; i < S::NW; i++)
-      load_lds<16>(wr, S::SB * st + wk[i] < nblk ? wo[i] + st * S::WB : kOOB,
+      lds_load<16>(wr, S::SB * st + wk[i] < nblk ? wo[i] + st * S::WB : kOutOfRange,
                    base + S::W0 + (i * S::T + wave * 64) * 16);
 #pragma unroll
     for (int i = 0; i < S::NS; i++) {
-      const uint32_t off = S::SB * st + sk[i] < nblk ? so[i] + st * S::SB : kOOB;
-      load_lds<(S::MX && !S::BYTE_SCALES) ? 4 : 1>(s_is_x[i] ? xsr : wsr, off,
+      const uint32_t off = S::SB * st + sk[i] < nblk ? so[i] + st * S::SB : kOutOfRange;
+      lds_load<(S::MX && !S::BYTE_SCALES) ? 4 : 1>(s_is_x[i] ? xsr : wsr, off,
                                                    base + S::S0 + (i * S::T + wave * 64) * 4);
     }
   };
@@ -240,7 +198,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   for (int i = 0; i < S::D - 1; i++) issue(i, i);
   int buf = 0;
   for (int st = 0; st < steps; st++) {
-    wait_barrier<(S::D - 2) * S::LOADS>();
+    wait_loads_barrier<(S::D - 2) * S::LOADS>();
     issue(st + S::D - 1, buf == 0 ? S::D - 1 : buf - 1);
     const uint8_t* xs = smem + buf * S::STAGE + S::X0;
     const uint8_t* wl = smem + buf * S::STAGE + S::W0;
@@ -287,7 +245,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     }
     buf = buf + 1 == S::D ? 0 : buf + 1;
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing writes LDS after the workgroup
+  wait_loads<0>();  // nothing writes LDS after the workgroup
 
 #pragma unroll
   for (int x = 0; x < S::TX; x++) {
@@ -351,13 +309,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
       }
       continue;
     }
-    uint32_t amax = 0u;
-#pragma unroll
-    for (int i = 0; i < 2 * P; i++) {
-      const uint32_t lo = (h[i] & 0x7FFFu) << 16, hi = h[i] & 0x7FFF0000u;
-      amax = amax > lo ? amax : lo;
-      amax = amax > hi ? amax : hi;
-    }
+    uint32_t amax = amax_pairs<2 * P>(h);
     uint32_t o = __shfl_xor(amax, 16, 64);
     amax = amax > o ? amax : o;
     if (P == 2) {
@@ -368,19 +320,8 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     const bool bad = amax >= 0x7F800000u;
     uint32_t code[P / 2];
 #pragma unroll
-    for (int i = 0; i < P / 2; i++) {
-      float q[8];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        q[2 * j] = __builtin_ldexpf(__uint_as_float(h[4 * i + j] << 16), 127 - (int)sc);
-        q[2 * j + 1] = __builtin_ldexpf(__uint_as_float(h[4 * i + j] & 0xFFFF0000u), 127 - (int)sc);
-      }
-      uint32_t v = e2m1_rne2<0>(0u, q[0], q[1]);
-      v = e2m1_rne2<1>(v, q[2], q[3]);
-      v = e2m1_rne2<2>(v, q[4], q[5]);
-      v = e2m1_rne2<3>(v, q[6], q[7]);
-      code[i] = bad ? 0u : v;
-    }
+    for (int i = 0; i < P / 2; i++)
+      code[i] = bad ? 0u : codes_of_pairs(h[4 * i], h[4 * i + 1], sc) | codes_of_pairs(h[4 * i + 2], h[4 * i + 3], sc) << 16;
     if (!ok || n >= half) continue;  // blocks end where the columns do
     uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + row * (half >> 1) + (n >> 1));
 #pragma unroll
@@ -390,10 +331,10 @@ void mx_tiled(MxArgs a, int gm, int vec) {
 }
 
 template <class S>
-hipError_t launch_shape(const MxArgs& a, int64_t max_tiles, hipStream_t stream) {
+hipError_t launch_shape(const MxArgs& a, hipStream_t stream) {
   const int64_t bc = a.swiglu ? S::BN / 2 : S::BN;
   const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
-  const int64_t nbm = a.tiles ? max_tiles : (a.M + S::BM - 1) / S::BM;
+  const int64_t nbm = a.tiles ? a.max_tiles : (a.M + S::BM - 1) / S::BM;
   const int64_t groups = nbm * ((cols + bc - 1) / bc);
   if (groups * S::T > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
   const int gm = S::MX ? 4 : 2;
@@ -409,26 +350,24 @@ hipError_t launch_shape(const MxArgs& a, int64_t max_tiles, hipStream_t stream) 
 
 }  // namespace
 
-bool mx_tiled_takes(const MxArgs& a, int act_kind) {
-  // 32-bit offsets into the activations (dense: from the tile's first row) and one weight
-  const int64_t pitch = act_kind == MXFP4_ACT_MXFP4 ? a.K >> 1 : a.ldx * 2;
-  const int64_t rows = a.tiles ? a.x_rows : (a.M < 256 ? a.M : 256);
-  return rows * pitch < (int64_t)kOOB && a.N * (a.K >> 1) < (int64_t)kOOB;
-}
-
-hipError_t launch_mx_tiled(const MxArgs& a, int act_kind, int64_t max_tiles, hipStream_t stream) {
-  const bool wide = !a.tiles;
-  if (act_kind == MXFP4_ACT_BF16) {
-    if (wide) return launch_shape<Shape<MXFP4_ACT_BF16, 256, 256, 4, 2, 3, false>>(a, max_tiles, stream);
-    return launch_shape<Shape<MXFP4_ACT_BF16, 128, 256, 4, 2, 4, false>>(a, max_tiles, stream);
-  }
+hipError_t launch_mx_tiled(const MxArgs& a, int act_kind, hipStream_t stream) {
   const bool dwords = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.w_scales) % 4 == 0;
-  if (wide) {
-    if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 256, 256, 2, 4, 4, false>>(a, max_tiles, stream);
-    return launch_shape<Shape<MXFP4_ACT_MXFP4, 256, 256, 2, 4, 3, true>>(a, max_tiles, stream);
+  const int64_t rows = a.tiles ? a.tile_rows : a.M;
+  if (act_kind == MXFP4_ACT_BF16) {
+    if (rows <= 64) return launch_shape<Shape<MXFP4_ACT_BF16, 64, 256, 2, 4, 4, false>>(a, stream);
+    if (rows <= 128) return launch_shape<Shape<MXFP4_ACT_BF16, 128, 256, 4, 2, 4, false>>(a, stream);
+    return launch_shape<Shape<MXFP4_ACT_BF16, 256, 256, 4, 2, 3, false>>(a, stream);
   }
-  if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 128, 256, 2, 4, 4, false>>(a, max_tiles, stream);
-  return launch_shape<Shape<MXFP4_ACT_MXFP4, 128, 256, 2, 4, 4, true>>(a, max_tiles, stream);
+  if (rows <= 64) {
+    if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 64, 256, 1, 4, 4, false>>(a, stream);
+    return launch_shape<Shape<MXFP4_ACT_MXFP4, 64, 256, 1, 4, 4, true>>(a, stream);
+  }
+  if (rows <= 128) {
+    if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 128, 256, 2, 4, 4, false>>(a, stream);
+    return launch_shape<Shape<MXFP4_ACT_MXFP4, 128, 256, 2, 4, 4, true>>(a, stream);
+  }
+  if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 256, 256, 2, 4, 4, false>>(a, stream);
+  return launch_shape<Shape<MXFP4_ACT_MXFP4, 256, 256, 2, 4, 3, true>>(a, stream);
 }
 
 }  // namespace nvfp4

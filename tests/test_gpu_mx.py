@@ -316,7 +316,8 @@ def route_rows(xv, w, ids, per_route):
 
 
 GROUPED = [(1, 4, 1, 64, 32), (1, 128, 8, 128, 2048), (16, 128, 8, 192, 256), (5, 3, 3, 130, 96), (40, 6, 2, 64, 1056),
-           (333, 24, 3, 66, 160), (200, 2, 1, 256, 512), (64, 300, 4, 128, 64), (700, 8, 2, 320, 288), (1500, 5, 2, 130, 128)]
+           (333, 24, 3, 66, 160), (200, 2, 1, 256, 512), (64, 300, 4, 128, 64), (700, 8, 2, 320, 288), (1500, 5, 2, 130, 128),
+           (100, 128, 4, 128, 160), (300, 64, 2, 66, 544), (256, 40, 1, 192, 64), (257, 40, 1, 64, 96), (90, 200, 64, 64, 32), (4, 70, 64, 64, 64)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
@@ -354,7 +355,7 @@ def test_grouped_routes_swiglu_combine(dev, T, E, k, N, K, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
-@pytest.mark.parametrize("T,E,k", [(9, 7, 3), (300, 7, 3), (2500, 4, 2)])
+@pytest.mark.parametrize("T,E,k", [(9, 7, 3), (120, 40, 5), (300, 7, 3), (2500, 4, 2)])
 def test_grouped_bad_routes(dev, T, E, k, kind):
     """Ids out of range and repeated: flagged, their rows zero, the others as without them."""
     N, K = 128, 96
@@ -391,7 +392,8 @@ def test_grouped_all_on_one_expert_and_one_row_each(dev):
     rng = rng_of(12)
     c, s = weight(rng, E, N, K)
     w = ref.dequantize(c, s)
-    for ids in (np.full((259, 1), 17, np.int32), np.arange(E, dtype=np.int32)[:, None]):
+    for ids in (np.full((200, 1), 39, np.int32), np.full((259, 1), 17, np.int32), np.full((2000, 1), 0, np.int32),
+                np.arange(E, dtype=np.int32)[:, None]):
         x = acts(rng, ids.shape[0], K)
         y, mag, _ = route_rows(num(x), w, ids, False)
         got = nv.mxfp4_grouped_linear(x.to(dev), up(c, dev), up(s, dev), up(ids, dev))
@@ -539,7 +541,7 @@ def test_binding_refusals(dev):
         (lambda: nv.mxfp4_grouped_linear(x, c[None], s[None], ids, out_mode=nv.OUT_COMBINE), "NULL"),
         (lambda: nv.mxfp4_grouped_linear(x, c[None], s[None], ids, out_mode=nv.OUT_SWIGLU_MXFP4), "SHAPE"),
         (lambda: nv.mxfp4_grouped_linear(x, c[None], s[None], ids, out_mode=nv.OUT_SWIGLU_BF16, out_dtype=torch.float32), "ARG"),
-        (lambda: nv.mxfp4_grouped_linear(x, c[None], s[None], ids, workspace=torch.empty(256, **u8)), "WORKSPACE"),
+        (lambda: nv.mxfp4_grouped_linear(x, c[None], s[None], ids, workspace=torch.empty(128, **u8)), "WORKSPACE"),
         (lambda: nv.mxfp4_grouped_linear(x, c[None], s[None], torch.zeros((4, 2), dtype=torch.int32, device=dev)), "ARG"),
     ):
         with pytest.raises(nv.NVFP4Error, match=name):

@@ -63,7 +63,7 @@ def test_dequantize_refusals(lib, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(K=0), ERR_SHAPE), (dict(K=48), ERR_SHAPE), (dict(M=0), ERR_SHAPE), (dict(N=0), ERR_SHAPE), (dict(M=1 << 31), ERR_SHAPE),
     (dict(N=1 << 31), ERR_SHAPE), (dict(act=2), ERR_ARG), (dict(act=-1), ERR_ARG), (dict(t=2), ERR_ARG), (dict(x=None), ERR_NULL),
-    (dict(x=P + 8), ERR_ALIGN), (dict(ldx=4000), ERR_SHAPE), (dict(ldx=4100), ERR_ALIGN), (dict(xs=P), ERR_ARG),
+    (dict(x=P + 8), ERR_ALIGN), (dict(ldx=4000), ERR_SHAPE), (dict(ldx=4100), ERR_ALIGN), (dict(ldx=1 << 29), ERR_SHAPE), (dict(xs=P), ERR_ARG),
     (dict(act=1), ERR_NULL), (dict(wc=None), ERR_NULL), (dict(ws=None), ERR_NULL), (dict(wc=P + 4), ERR_ALIGN),
     (dict(y=None), ERR_NULL), (dict(ldy=100), ERR_SHAPE), (dict(y=P + 2), ERR_ALIGN), (dict(t=0, y=P + 1), ERR_ALIGN),
     (dict(flags=2), ERR_ARG), (dict(flags=1), ERR_NULL), (dict(flags=1, f=P + 2), ERR_ALIGN), (dict(f=P + 1), ERR_ALIGN),
@@ -88,10 +88,11 @@ def grouped(lib, act=0, x=P, xs=None, ldx=2048, rows_mode=0, T=16, k=8, N=1536, 
     (dict(mode=0x100), ERR_ARG), (dict(mode=0x101, t=0), ERR_ARG), (dict(mode=0x103, t=0), ERR_ARG), (dict(mode=1, t=1), ERR_ARG),
     (dict(mode=3, t=1), ERR_ARG), (dict(T=0), ERR_SHAPE), (dict(N=0), ERR_SHAPE), (dict(K=2047), ERR_SHAPE),
     (dict(T=1 << 22, k=2), ERR_SHAPE), (dict(mode=1, t=0, N=1535), ERR_SHAPE), (dict(mode=3, t=0, N=1568, ys=P), ERR_SHAPE),
-    (dict(nbytes=1000), ERR_WORKSPACE), (dict(work=P + 16), ERR_ALIGN), (dict(x=None), ERR_NULL), (dict(ids=None), ERR_NULL),
+    (dict(nbytes=100), ERR_WORKSPACE), (dict(T=4096, nbytes=100000), ERR_WORKSPACE), (dict(mode=2, nbytes=1000), ERR_WORKSPACE), (dict(work=P + 16), ERR_ALIGN), (dict(x=None), ERR_NULL), (dict(ids=None), ERR_NULL),
     (dict(y=None), ERR_NULL), (dict(mode=2, tw=None), ERR_NULL), (dict(mode=3, t=0), ERR_NULL), (dict(ys=P), ERR_ARG),
     (dict(ids=P + 2), ERR_ALIGN), (dict(tw=P + 2), ERR_ALIGN), (dict(wc=P + 8), ERR_ALIGN), (dict(mode=3, t=0, ys=P, y=P + 8), ERR_ALIGN),
     (dict(y=P + 2), ERR_ALIGN), (dict(act=1), ERR_NULL), (dict(act=2), ERR_ARG), (dict(xs=P), ERR_ARG), (dict(ldx=2000), ERR_SHAPE),
+    (dict(ldx=1 << 27), ERR_SHAPE), (dict(N=1 << 22), ERR_SHAPE),  # beyond 32-bit offsets
     (dict(flags=2), ERR_ARG), (dict(flags=1), ERR_NULL), (dict(f=P + 2), ERR_ALIGN),
 ])
 def test_grouped_refusals(lib, kw, status):
