@@ -226,7 +226,8 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
   if (!aligned(y, out_mode == MXFP4_OUT_SWIGLU_MXFP4 ? 16 : (uintptr_t)type_bytes(y_type)))
     return NVFP4_ERR_ALIGN;
 
-  const int64_t R = T * top_k, xrows = rows_mode == NVFP4_ROWS_PER_TOKEN ? T : R;
+  const int64_t R = T * top_k, active = R < num_experts ? R : num_experts;
+  const int64_t xrows = rows_mode == NVFP4_ROWS_PER_TOKEN ? T : R;
   if (!fits(xrows, x_pitch(act_kind, ldx, K))) return NVFP4_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (flags & NVFP4_F_CHECK) {
@@ -261,7 +262,7 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
     ws.route_expert = ints(L.route_expert);
     ws.sorted = ints(L.sorted);
     ws.slots = ints(L.slots);
-    ws.max_slots = (int32_t)(R < num_experts ? R : num_experts);
+    ws.max_slots = (int32_t)active;
     ws.tiles = ints(L.tiles);
     ws.n_tiles = ints(L.n_tiles);
     ws.chunk_counts = ints(L.chunks);
@@ -280,7 +281,7 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
     a.tiles = ws.tiles; a.n_tiles = ws.n_tiles; a.offsets = ws.offsets; a.sorted = ws.sorted;
     a.slots = ws.slots; a.route_expert = ws.route_expert;
   }
-  e = plan.scan || plan.slots ? launch_mx_stream(a, act_kind, (R + num_experts - 1) / num_experts, s)
+  e = plan.scan || plan.slots ? launch_mx_stream(a, act_kind, (R + active - 1) / active, s)
                               : launch_mx_tiled(a, act_kind, s);
   if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
   if (out_mode == MXFP4_OUT_COMBINE)

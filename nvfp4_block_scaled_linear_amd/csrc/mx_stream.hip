@@ -143,30 +143,53 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
 // How a grouped workgroup finds its expert and the routes of it
 enum Mode {
   kDense,
-  kByExpert,  // few routes in all: the workgroup takes an expert and looks for it in topk_ids
+  kByExpert,  // few routes in all: the workgroup looks for its expert's routes in topk_ids
   kBySlot     // from the grouping: a slot record's first kMxSlotRoutes routes, or a list tile
 };
 constexpr int kScanRoutes = 256;  // kByExpert: routes in all, four per lane
 
-// bits of the routes 64 * i + lane that expert e keeps: those that hold e and are not a repeat
-// of it within their token (top_k <= 64: the token starts in this group of 64 or the last)
-__device__ __forceinline__ void scan_routes(const int32_t* ids, int R, int top_k, int e,
-                                            uint64_t (&kept)[kScanRoutes / 64]) {
+// The expert of workgroup group `group` and the bits of the routes 64 * i + lane that it keeps:
+// those that hold it and are not a repeat of it within their token (top_k <= 64: the token
+// starts in this group of 64 or the last). With fewer routes than experts the groups are the
+// routes, and the expert's first route is the one that takes it; returns whether there is work.
+__device__ __forceinline__ bool scan_routes(const int32_t* ids, int R, int top_k, int E, int group,
+                                            int* expert, uint64_t (&kept)[kScanRoutes / 64]) {
   const int lane = threadIdx.x & 63;
   int32_t id[kScanRoutes / 64];
 #pragma unroll
   for (int i = 0; i < kScanRoutes / 64; i++) id[i] = 64 * i + lane < R ? ids[64 * i + lane] : -1;
+  int e = group;
+  if (R < E) {
+#pragma unroll
+    for (int i = 0; i < kScanRoutes / 64; i++)
+      if (i == group / 64) e = __builtin_amdgcn_readlane(id[i], group % 64);
+    if (e < 0 || e >= E) return false;
+  }
+  *expert = e;
   uint64_t last = 0u;
 #pragma unroll
   for (int i = 0; i < kScanRoutes / 64; i++) {
     const uint64_t m = __ballot(id[i] == e);
-    const int before = (64 * i + lane) % top_k;  // routes of the token before this one
-    // bit 63: the route before this one, bit 62 the one before that, ...
-    const uint64_t window = (lane ? m << (64 - lane) : 0u) | last >> lane;
-    const bool repeat = before && (window >> (64 - before)) != 0u;
-    kept[i] = __ballot(id[i] == e && !repeat);
+    kept[i] = m;
+    if (__builtin_popcountll(m) + (last != 0u) > 1) {  // there may be repeats
+      const int before = (64 * i + lane) % top_k;      // routes of the token before this one
+      // bit 63: the route before this one, bit 62 the one before that, ...
+      const uint64_t window = (lane ? m << (64 - lane) : 0u) | last >> lane;
+      const bool repeat = before && (window >> (64 - before)) != 0u;
+      kept[i] = __ballot(id[i] == e && !repeat);
+    }
     last = m;
   }
+  // R < E: no route before this one, and this one, is the expert's
+  bool work = true;
+  if (R < E) {
+#pragma unroll
+    for (int i = 0; i < kScanRoutes / 64; i++) {
+      const uint64_t below = i < group / 64 ? ~0ull : i == group / 64 ? (1ull << group % 64) - 1 : 0ull;
+      work = work && (kept[i] & below) == 0u;
+    }
+  }
+  return work;
 }
 
 template <class C, int MODE, int SWIGLU>
@@ -179,21 +202,20 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
   __shared__ int32_t route_list[C::W][16];  // the pass's routes, a copy for each wave
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t N = a.N, K = a.K, half = N >> 1;
-  const int64_t cols = SWIGLU ? half : N;
-  const int nb = (int)(K >> 5);
-  const int64_t nbn = (cols + 16 * NO - 1) / (16 * NO);
-  const int64_t n0 = (blockIdx.x % nbn) * (16 * NO);
+  // sizes below 2^31 (a weight's bytes too): 32-bit arithmetic
+  const int N = (int)a.N, half = N >> 1, cols = SWIGLU ? half : N;
+  const int nb = (int)(a.K >> 5), wpitch = 16 * nb;
+  const uint32_t nbn = (cols + 16 * NO - 1) / (16 * NO);
   const int group = (int)(blockIdx.x / nbn);
+  const int n0 = (int)(blockIdx.x - group * nbn) * (16 * NO);
   const uint8_t* wc = a.w_codes;
   const uint8_t* wsc = a.w_scales;
   int count = (int)a.M, first = 0, e = 0;  // rows; bySlot: their place in `sorted`
   int32_t my_route = 0;                    // bySlot: routes of the first pass
   uint64_t kept[kScanRoutes / 64];
   if (MODE == kByExpert) {
-    e = group;
     if (blockIdx.x == 0) drop_routes<SWIGLU>(a);
-    scan_routes(a.ids, (int)a.R, a.top_k, e, kept);
+    if (!scan_routes(a.ids, (int)a.R, a.top_k, a.num_experts, group, &e, kept)) return;
     count = 0;
 #pragma unroll
     for (int i = 0; i < kScanRoutes / 64; i++) count += __builtin_popcountll(kept[i]);
@@ -222,32 +244,32 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
     }
   }
   if (GROUPED) {
-    wc += (int64_t)e * N * (K >> 1);
+    wc += (int64_t)e * N * wpitch;
     wsc += (int64_t)e * N * nb;
   }
   Operands d;
-  const int64_t r0 = SWIGLU ? 0 : n0;  // weight row that the offsets count from
-  d.w = lds_load_rsrc(wc + r0 * (K >> 1), (N - r0) * (K >> 1));
-  d.ws = lds_load_rsrc(wsc + r0 * nb, (N - r0) * nb);
-  const int64_t xpitch = C::MX ? K >> 1 : a.ldx * 2;
-  d.x = lds_load_rsrc(a.x, (a.x_rows - 1) * xpitch + (C::MX ? K >> 1 : 2 * K));
+  const int r0 = SWIGLU ? 0 : n0;  // weight row that the offsets count from
+  d.w = lds_load_rsrc(wc + (int64_t)r0 * wpitch, (int64_t)(N - r0) * wpitch);
+  d.ws = lds_load_rsrc(wsc + (int64_t)r0 * nb, (int64_t)(N - r0) * nb);
+  const uint32_t xpitch = C::MX ? wpitch : (uint32_t)a.ldx * 2;
+  d.x = lds_load_rsrc(a.x, (a.x_rows - 1) * xpitch + (C::MX ? wpitch : 4 * wpitch));
   d.xs = C::MX ? lds_load_rsrc(a.x_scales, a.x_rows * nb) : d.x;
   // row i of weight tile t, from r0, or -1
-  const auto w_row = [&](int t, int i) -> int64_t {
-    const int64_t n = n0 + 16 * (t % NO) + i;
+  const auto w_row = [&](int t, int i) {
+    const int n = n0 + 16 * (t % NO) + i;
     return n < cols ? n - r0 + (t >= NO ? half : 0) : -1;
   };
   const int wq = (lane & 3) ^ ((lane >> 4) & 3);
   uint32_t wo[C::NT], wso[C::SW];
 #pragma unroll
   for (int t = 0; t < C::NT; t++) {
-    const int64_t row = w_row(t, lane >> 2);
-    wo[t] = row >= 0 ? (uint32_t)(row * (K >> 1)) + 16 * wq : kOutOfRange;
-    if (!C::DW) wso[t] = row >= 0 ? (uint32_t)(row * nb) + (lane & 3) : kOutOfRange;
+    const int row = w_row(t, lane >> 2);
+    wo[t] = row >= 0 ? (uint32_t)row * wpitch + 16 * wq : kOutOfRange;
+    if (!C::DW) wso[t] = row >= 0 ? (uint32_t)row * nb + (lane & 3) : kOutOfRange;
   }
   if (C::DW) {
-    const int64_t row = (lane >> 4) < C::NT ? w_row(lane >> 4, c) : -1;
-    wso[0] = row >= 0 ? (uint32_t)(row * nb) : kOutOfRange;
+    const int row = (lane >> 4) < C::NT ? w_row(lane >> 4, c) : -1;
+    wso[0] = row >= 0 ? (uint32_t)row * nb : kOutOfRange;
   }
   // this wave's steps: a run of an even number (two steps are one 128-byte line of codes)
   const int steps = (nb + 3) >> 2;
@@ -274,23 +296,23 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
     }
     if (GROUPED) __builtin_amdgcn_wave_barrier();
     // output row of the pass's i-th row, and its x row or -1
-    const auto y_row = [&](int i) -> int64_t { return GROUPED ? list[i] : p0 + i; };
-    const auto x_row = [&](int i) -> int64_t {
+    const auto y_row = [&](int i) { return GROUPED ? list[i] : p0 + i; };
+    const auto x_row = [&](int i) {
       if (i >= rows) return -1;
-      const int64_t r = y_row(i);
-      return GROUPED && a.rows_per_token ? r / a.top_k : r;
+      const int r = y_row(i);
+      return GROUPED && a.rows_per_token ? (int)((uint32_t)r / (uint32_t)a.top_k) : r;
     };
     uint32_t xo[C::XMAX], xso[C::SX > 0 ? C::SX : 1];
 #pragma unroll
     for (int i = 0; i < C::XMAX; i++) {
-      const int64_t row = x_row(C::MX ? 16 * i + (lane >> 2) : 4 * i + (lane >> 4));
+      const int row = x_row(C::MX ? 16 * i + (lane >> 2) : 4 * i + (lane >> 4));
       const int q = C::MX ? wq : (lane & 15) ^ ((4 * i + (lane >> 4)) & 15);
-      xo[i] = row >= 0 ? (uint32_t)(row * xpitch) + 16 * q : kOutOfRange;
-      if (C::MX && !C::DW) xso[i] = row >= 0 ? (uint32_t)(row * nb) + (lane & 3) : kOutOfRange;
+      xo[i] = row >= 0 ? (uint32_t)row * xpitch + 16 * q : kOutOfRange;
+      if (C::MX && !C::DW) xso[i] = row >= 0 ? (uint32_t)row * nb + (lane & 3) : kOutOfRange;
     }
     if (C::MX && C::DW) {
-      const int64_t row = (lane >> 4) < C::TM ? x_row(lane) : -1;
-      xso[0] = row >= 0 ? (uint32_t)(row * nb) : kOutOfRange;
+      const int row = (lane >> 4) < C::TM ? x_row(lane) : -1;
+      xso[0] = row >= 0 ? (uint32_t)row * nb : kOutOfRange;
     }
     f32x4 acc[C::NT][C::TM];
 #pragma unroll
@@ -317,7 +339,7 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
       const int t = i % (NO / TS) * TS, x = i / (NO / TS);
       const bool ok = 16 * x + c < rows;
       const int64_t row = ok ? y_row(16 * x + c) : 0;
-      const int64_t n = n0 + 16 * t + 4 * g;
+      const int n = n0 + 16 * t + 4 * g;
       const f32x4 v = total(t, x);
       if (!SWIGLU) {
         if (!ok) continue;
@@ -382,7 +404,7 @@ hipError_t launch_mode(const MxArgs& a, int64_t groups, hipStream_t stream) {
 template <class C>
 hipError_t launch_cfg(const MxArgs& a, hipStream_t stream) {
   if constexpr (C::TM == 1) {
-    if (a.ids) return launch_mode<C, kByExpert>(a, a.num_experts, stream);
+    if (a.ids) return launch_mode<C, kByExpert>(a, a.R < a.num_experts ? a.R : a.num_experts, stream);
     if (a.slots) return launch_mode<C, kBySlot>(a, a.max_slots + a.max_tiles, stream);
   }
   return launch_mode<C, kDense>(a, 1, stream);
@@ -396,10 +418,23 @@ hipError_t launch_rows(const MxArgs& a, hipStream_t stream) {
             : launch_cfg<Cfg<ACT, XR, NT, W, U, false>>(a, stream);
 }
 
+template <int ACT, int XR, int U>
+hipError_t launch_dense(const MxArgs& a, hipStream_t stream) {
+  const int64_t nt = (a.N + 16 * 256 - 1) / (16 * 256);  // so that a CU has about one workgroup
+  if (nt <= 1) return launch_rows<ACT, XR, 1, 4, U>(a, stream);
+  if (nt <= 2) return launch_rows<ACT, XR, 2, 4, U>(a, stream);
+  return launch_rows<ACT, XR, 3, 4, U>(a, stream);
+}
+
 template <int ACT>
 hipError_t launch_act(const MxArgs& a, int64_t rows, hipStream_t stream) {
-  if (a.swiglu) return launch_rows<ACT, 16, 4, 4, 2>(a, stream);
-  if (rows <= 16) return launch_rows<ACT, 16, 2, 4, 2>(a, stream);
+  constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
+  if (a.ids || a.slots) {
+    if (a.swiglu) return rows <= 2 ? launch_rows<ACT, MX ? 16 : 4, 4, 4, 2>(a, stream) : launch_rows<ACT, 16, 4, 4, 2>(a, stream);
+    return rows <= 2 ? launch_rows<ACT, MX ? 16 : 4, 2, 2, 2>(a, stream) : launch_rows<ACT, 16, 2, 2, 2>(a, stream);
+  }
+  if (rows <= 4) return launch_dense<ACT, MX ? 16 : 4, MX ? 4 : 2>(a, stream);
+  if (rows <= 16) return launch_dense<ACT, 16, MX ? 4 : 2>(a, stream);
   if (rows <= 32) return launch_rows<ACT, 32, 2, 4, 2>(a, stream);
   return launch_rows<ACT, 64, 2, 4, 2>(a, stream);
 }

@@ -348,26 +348,39 @@ hipError_t launch_shape(const MxArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+constexpr int64_t kFewTiles = 200;
+
+//LAUNCH
+template <int ACT, int BM, int BN, int WX, int WW, int D>
+hipError_t launch_scales(const MxArgs& a, bool dwords, hipStream_t stream) {
+  if constexpr (ACT == MXFP4_ACT_MXFP4) {
+    if (!dwords) return launch_shape<Shape<ACT, BM, BN, WX, WW, (D > 3 ? D - 1 : D), true>>(a, stream);
+  }
+  return launch_shape<Shape<ACT, BM, BN, WX, WW, D, false>>(a, stream);
+}
+
+template <int ACT>
+hipError_t launch_act(const MxArgs& a, hipStream_t stream) {
+  constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
+  const bool dwords = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.w_scales) % 4 == 0;
+  const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
+  // workgroups that tiles of bm rows and bn weight rows make
+  const auto tiles = [&](int64_t bm, int64_t bn) {
+    const int64_t bc = a.swiglu ? bn / 2 : bn;
+    return (a.tiles ? a.max_tiles : (a.M + bm - 1) / bm) * ((cols + bc - 1) / bc);
+  };
+  const int64_t rows = a.tiles ? a.tile_rows : a.M;
+  if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_scales<ACT, 256, 256, MX ? 2 : 4, MX ? 4 : 2, MX ? 4 : 3>(a, dwords, stream);
+  if (rows > 64 && tiles(128, 256) >= kFewTiles) return launch_scales<ACT, 128, 256, MX ? 2 : 4, MX ? 4 : 2, 4>(a, dwords, stream);
+  if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_scales<ACT, 128, 128, 2, 2, 4>(a, dwords, stream);
+  return launch_scales<ACT, 64, 128, 2, 2, 4>(a, dwords, stream);
+}
+//END
+
 }  // namespace
 
 hipError_t launch_mx_tiled(const MxArgs& a, int act_kind, hipStream_t stream) {
-  const bool dwords = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.w_scales) % 4 == 0;
-  const int64_t rows = a.tiles ? a.tile_rows : a.M;
-  if (act_kind == MXFP4_ACT_BF16) {
-    if (rows <= 64) return launch_shape<Shape<MXFP4_ACT_BF16, 64, 256, 2, 4, 4, false>>(a, stream);
-    if (rows <= 128) return launch_shape<Shape<MXFP4_ACT_BF16, 128, 256, 4, 2, 4, false>>(a, stream);
-    return launch_shape<Shape<MXFP4_ACT_BF16, 256, 256, 4, 2, 3, false>>(a, stream);
-  }
-  if (rows <= 64) {
-    if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 64, 256, 1, 4, 4, false>>(a, stream);
-    return launch_shape<Shape<MXFP4_ACT_MXFP4, 64, 256, 1, 4, 4, true>>(a, stream);
-  }
-  if (rows <= 128) {
-    if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 128, 256, 2, 4, 4, false>>(a, stream);
-    return launch_shape<Shape<MXFP4_ACT_MXFP4, 128, 256, 2, 4, 4, true>>(a, stream);
-  }
-  if (dwords) return launch_shape<Shape<MXFP4_ACT_MXFP4, 256, 256, 2, 4, 4, false>>(a, stream);
-  return launch_shape<Shape<MXFP4_ACT_MXFP4, 256, 256, 2, 4, 3, true>>(a, stream);
+  return act_kind == MXFP4_ACT_BF16 ? launch_act<MXFP4_ACT_BF16>(a, stream) : launch_act<MXFP4_ACT_MXFP4>(a, stream);
 }
 
 }  // namespace nvfp4
