@@ -20,8 +20,11 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 
 # Per-source flags. The weight-streaming kernels feed every 4x4x4 MFMA result straight
 # into VALU FMAs (the per-block scale); in the accumulation-register form each of those
-# reads costs one v_accvgpr_read, so their MFMAs write ordinary VGPRs.
-EXTRA = {"stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# reads costs one v_accvgpr_read, so their MFMAs write ordinary VGPRs. The MXFP4 kernels'
+# scaled MFMAs in the accumulation-register form get their accumulators copied around in
+# every step.
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+EXTRA = {f: _VGPR_FORM for f in ("stream.hip", "mx_stream.hip", "mx_tiled.hip")}
 
 
 def sources() -> list[str]:

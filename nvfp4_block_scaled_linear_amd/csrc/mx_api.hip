@@ -273,8 +273,9 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
       const bool keep = out_mode == MXFP4_OUT_COMBINE;
       const int64_t row_bytes = out_mode == MXFP4_OUT_ROUTES ? N * type_bytes(y_type)
                                 : out_mode == MXFP4_OUT_SWIGLU_BF16 ? N : N / 4;
-      e = launch_route_sort(topk_ids, T, top_k, num_experts, ws, faults, keep ? nullptr : y,
-                            row_bytes, s);
+      e = R <= kMxGroupRoutes
+              ? launch_mx_group(topk_ids, R, top_k, num_experts, ws, faults, keep ? nullptr : y, row_bytes, s)
+              : launch_route_sort(topk_ids, T, top_k, num_experts, ws, faults, keep ? nullptr : y, row_bytes, s);
       if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
     }
     a.tile_rows = plan.tile_rows; a.max_tiles = plan.max_tiles; a.max_slots = ws.max_slots;
@@ -285,7 +286,7 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
                               : launch_mx_tiled(a, act_kind, s);
   if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
   if (out_mode == MXFP4_OUT_COMBINE)
-    e = launch_mx_combine(rows, topk_ids, topk_w, T, top_k, num_experts, N, y_type, y, s);
+    e = launch_mx_combine(rows, N, topk_ids, topk_w, T, top_k, num_experts, N, y_type, y, N, s);
   return launch_status(e);
 }
 

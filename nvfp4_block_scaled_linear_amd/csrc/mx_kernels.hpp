@@ -62,10 +62,18 @@ hipError_t launch_mx_stream(const MxArgs& a, int act_kind, int64_t rows, hipStre
 int64_t mx_scan_routes();
 constexpr int kMxSlotRoutes = 16;
 
-// y[t] = sum over t's kept routes in ascending expert id of topk_w * rows[route]
-hipError_t launch_mx_combine(const float* rows, const int32_t* topk_ids, const float* topk_w,
-                             int64_t T, int top_k, int E, int64_t N, int y_type, void* y,
-                             hipStream_t stream);
+// groups up to kMxGroupRoutes routes; what launch_route_sort writes, and it clears dropped rows
+constexpr int kMxGroupRoutes = 4096;
+hipError_t launch_mx_group(const int32_t* topk_ids, int64_t R, int top_k, int E,
+                           const RouteWorkspace& ws, uint32_t* faults, void* zero_out,
+                           int64_t zero_row_bytes, hipStream_t stream);
+
+// y[t] = sum over t's kept routes in ascending expert id of topk_w * rows[route], N columns of
+// rows of `pitch` and ldy values
+hipError_t launch_mx_combine(const float* rows, int64_t pitch, const int32_t* topk_ids,
+                             const float* topk_w, int64_t T, int top_k, int E, int64_t N,
+                             int y_type, void* y, int64_t ldy, hipStream_t stream);
+
 // check mode: scale bytes 0xFF in [0, bytes) set NVFP4_FAULT_NAN_SCALE
 hipError_t launch_mx_check_scales(const uint8_t* scales, int64_t bytes, uint32_t* faults,
                                   hipStream_t stream);

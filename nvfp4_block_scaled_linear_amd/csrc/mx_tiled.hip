@@ -8,8 +8,8 @@
 //    compiler does not wait for; one counted wait and one barrier per stage stand before its
 //    reads. Past the end of K (and of the rows) the loads are out of range and write zeros,
 //    so every stage issues the same number and the count holds to the last one.
-//  - A stage is 128 k of codes for MXFP4 activations (64 bytes a row on both sides), 64 k for
-//    BF16 ones (128 bytes of activations, 32 of codes).
+//  - A stage is 256 k of codes for MXFP4 activations (128 bytes, a cache line, of a row on both
+//    sides), 64 k for BF16 ones (128 bytes of activations, 32 of codes).
 //  - LDS rows have no padding (the loads write 1 KiB runs); 16-byte piece q of a row lies at
 //    slot q ^ f(row), with f such that the 16 rows that lanes read together fall into
 //    different banks.
@@ -17,6 +17,8 @@
 //    16-row tile (P tiles to a group): a lane's results are then 4P consecutive columns, so
 //    it stores 16 bytes at a time and holds a block's half or quarter when SwiGLU's result is
 //    quantized.
+#include <type_traits>
+
 #include "mx_device.hpp"
 #include "mx_kernels.hpp"
 #include "mx_routes.hpp"
@@ -24,28 +26,47 @@
 namespace nvfp4 {
 namespace {
 
-template <int ACT_, int BM_, int BN_, int WX_, int WW_, int D_, bool BYTE_SCALES_>
+// How the scales are loaded. A load costs by the cache lines it looks up, and every row is one,
+// so windows of 16 bytes a row (512 k) are taken where rows are aligned to them; otherwise a
+// dword a row for 128 k (MXFP4 activations), or a byte per row and block.
+enum Scales { kBytes, kDwords, kWindows };
+
+template <int ACT_, int BM_, int BN_, int WX_, int WW_, int D_, int SCALES_>
 struct Shape {
-  static constexpr int ACT = ACT_, BM = BM_, BN = BN_, WX = WX_, WW = WW_, D = D_;
-  // MXFP4 activations: scales loaded one byte per lane (any K, any alignment), or one dword
-  // per row and stage (K % 128 == 0, dword-aligned scales)
-  static constexpr bool BYTE_SCALES = BYTE_SCALES_;
+  static constexpr int ACT = ACT_, BM = BM_, BN = BN_, WX = WX_, WW = WW_, D = D_, SCALES = SCALES_;
   static constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
   static constexpr int T = 64 * WX * WW;
   static constexpr int TX = BM / WX / 16, TW = BN / WW / 16;
-  static constexpr int XB = MX ? 64 : 128, WB = MX ? 64 : 32;  // bytes of a row per stage
-  static constexpr int SB = MX ? 4 : 2;                        // weight blocks per stage
+  static constexpr int XB = 128, WB = MX ? 128 : 32;  // bytes of a row per stage
+  static constexpr int SB = MX ? 8 : 2;               // weight blocks per stage
   static constexpr int NX = BM * XB / (16 * T), NW = BN * WB / (16 * T);
-  // scale loads: BF16 activations BN * 2 bytes, one per lane; MXFP4 BM + BN rows
-  static constexpr int NS = !MX ? (BN * 2 + T - 1) / T
-                                : ((BM + BN) * (BYTE_SCALES ? 4 : 1) + T - 1) / T;
+  // rows with scales: the weight's, and MXFP4 activations'. Scale loads of a stage: windows,
+  // one load in WS stages (in the others it is out of range); otherwise for each 128 k half of
+  // MXFP4 activations' stage, or for the stage
+  static constexpr int ROWS = MX ? BM + BN : BN, WS = MX ? 2 : 8;
+  static constexpr int PER = SCALES == kBytes ? (MX ? 4 : 2) : 1;  // loads of a row and half
+  static constexpr int NH = (ROWS * PER + T - 1) / T;
+  static constexpr int NS = MX && SCALES != kWindows ? 2 * NH : NH;
   static constexpr int LOADS = NX + NW + NS;
-  static constexpr int X0 = 0, W0 = BM * XB, S0 = W0 + BN * WB, STAGE = S0 + NS * T * 4;
-  static constexpr int LDS = D * STAGE;
+  static constexpr int X0 = 0, W0 = BM * XB, S0 = W0 + BN * WB;
+  static constexpr int STAGE = S0 + (SCALES == kWindows ? 0 : NS * T * 4);
+  static constexpr int WIN0 = D * STAGE, WIN = SCALES == kWindows ? NS * T * 16 : 0;  // two windows
+  static constexpr int SINK = WIN0 + 2 * WIN;  // where loads go whose bytes nobody reads
+  static constexpr int LDS = SINK + 1024;
+  static_assert(SCALES != kWindows || D <= WS + 1, "a window is overwritten two windows later");
+  static_assert(SCALES != kDwords || MX, "");
   static_assert(NX * 16 * T == BM * XB && NW * 16 * T == BN * WB, "whole loads only");
   static_assert(LDS <= 160 * 1024, "LDS");
   static_assert(TW % 4 == 0, "weight rows come in groups of 64 (SwiGLU: 32 + 32)");
 };
+
+// bytes g, 4 + g, 8 + g and 12 + g of row r's 16 in a window
+__device__ __forceinline__ uint32_t window_bytes(const uint8_t* win, int r, int g) {
+  const u32x4 v = *reinterpret_cast<const u32x4*>(win + r * 16);
+  const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], 0x0400u + 0x0101u * (uint32_t)g);
+  const uint32_t hi = __builtin_amdgcn_perm(v[3], v[2], 0x0400u + 0x0101u * (uint32_t)g);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
 
 template <class S, bool GROUPED, int SWIGLU>
 __global__ __launch_bounds__(S::T) __attribute__((amdgpu_waves_per_eu(S::T == 512 ? 2 : 1, 2)))
@@ -112,14 +133,16 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     return n0 + u < half ? n0 + u + (t >= BC ? half : 0) : -1;
   };
 
+  const auto w_swizzle = [](int t) { return ((t >> 1) & 1) | ((t / (4 * P)) & 3) << 1; };
+
   // this lane's loads of stage 0; a stage on, offsets grow by XB / WB / SB bytes
   uint32_t xo[S::NX], wo[S::NW], so[S::NS];
   int xk[S::NX], wk[S::NW], sk[S::NS];  // first block (BF16 x: first 8-value piece) of the load
 #pragma unroll
   for (int i = 0; i < S::NX; i++) {
     const int p = i * S::T + tid;
-    const int r = S::MX ? p >> 2 : p >> 3;
-    const int q = S::MX ? (p & 3) ^ ((r >> 2) & 3) : (p & 7) ^ ((r >> 1) & 7);
+    const int r = p >> 3;
+    const int q = (p & 7) ^ ((r >> 1) & 7);
     xk[i] = q;
     xo[i] = r < rows_m ? (uint32_t)(x_row(r) * xpitch) + 16 * q : kOutOfRange;
   }
@@ -128,8 +151,8 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     const int p = i * S::T + tid;
     int t, q;
     if (S::MX) {
-      t = p >> 2;
-      q = (p & 3) ^ ((t / (4 * P)) & 3);
+      t = p >> 3;
+      q = (p & 7) ^ w_swizzle(t);
     } else {  // piece q of the row that lane p % 16 of 16-row tile p / 32 reads
       const int u = p >> 5, s = u % P;
       q = (p >> 4) & 1;
@@ -141,23 +164,20 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   }
   const u32x4 wsr = lds_load_rsrc(ws + (SWIGLU ? 0 : n0 * nb), (N - (SWIGLU ? 0 : n0)) * nb);
   const u32x4 xsr = S::MX ? lds_load_rsrc(a.x_scales + (GROUPED ? 0 : m0 * nb), x_last * nb) : wsr;
-  // scale loads: p-th of the stage. BF16: weight row p / 2, block p % 2. MXFP4: rows of the
-  // weight, then of the activations, four blocks (one dword, or four byte loads) each. Whole
-  // waves read one side (BN is a multiple of 64), so the descriptor is uniform.
+  // scale loads: the p-th is block p % PER (a dword: all four; a window: all sixteen) of row p /
+  // PER, of the weight, then of the activations. Whole waves read one side (BN is a multiple
+  // of 64), so the descriptor is uniform.
   bool s_is_x[S::NS];
 #pragma unroll
   for (int i = 0; i < S::NS; i++) {
-    const int p = i * S::T + tid;
-    const int per = !S::MX ? 2 : (S::BYTE_SCALES ? 4 : 1);
-    const int t = p / per;
-    sk[i] = p % per;
+    const int p = (i % S::NH) * S::T + tid, t = p / S::PER;
+    sk[i] = p % S::PER + i / S::NH * 4;
     s_is_x[i] = S::MX && __builtin_amdgcn_readfirstlane(t) >= S::BN;
     int64_t row = -1;
     if (t < S::BN) row = w_row(t);
     else if (S::MX && t - S::BN < rows_m) row = x_row(t - S::BN);
     so[i] = row >= 0 ? (uint32_t)(row * nb) + sk[i] : kOutOfRange;
   }
-
   const uint32_t lds0 = lds_address(smem);
   const int nblk = (int)nb;
   const auto issue = [&](int st, int buf) {
@@ -165,7 +185,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
 #pragma unroll
     for (int i = 0; i < S::NX; i++) {
       // a BF16 piece is in range when its block is: pieces 4 per block
-      const int b = S::MX ? 4 * st + xk[i] : 2 * st + (xk[i] >> 2);
+      const int b = S::MX ? 8 * st + xk[i] : 2 * st + (xk[i] >> 2);
       lds_load<16>(xr, b < nblk ? xo[i] + st * S::XB : kOutOfRange, base + S::X0 + (i * S::T + wave * 64) * 16);
     }
 #pragma unroll
@@ -174,9 +194,16 @@ void mx_tiled(MxArgs a, int gm, int vec) {
                    base + S::W0 + (i * S::T + wave * 64) * 16);
 #pragma unroll
     for (int i = 0; i < S::NS; i++) {
-      const uint32_t off = S::SB * st + sk[i] < nblk ? so[i] + st * S::SB : kOutOfRange;
-      lds_load<(S::MX && !S::BYTE_SCALES) ? 4 : 1>(s_is_x[i] ? xsr : wsr, off,
-                                                   base + S::S0 + (i * S::T + wave * 64) * 4);
+      const u32x4 sr = s_is_x[i] ? xsr : wsr;
+      if (S::SCALES == kWindows) {
+        const int w = st / S::WS;
+        const bool now = st % S::WS == 0 && S::SB * st < nblk;
+        lds_load<16>(sr, now ? so[i] + 16 * w : kOutOfRange,
+                     now ? lds0 + S::WIN0 + (w & 1) * S::WIN + (i * S::T + wave * 64) * 16 : lds0 + S::SINK);
+      } else {
+        const uint32_t off = S::SB * st + sk[i] < nblk ? so[i] + st * S::SB : kOutOfRange;
+        lds_load<S::SCALES == kDwords ? 4 : 1>(sr, off, base + S::S0 + (i * S::T + wave * 64) * 4);
+      }
     }
   };
 
@@ -197,31 +224,54 @@ void mx_tiled(MxArgs a, int gm, int vec) {
 #pragma unroll
   for (int i = 0; i < S::D - 1; i++) issue(i, i);
   int buf = 0;
-  for (int st = 0; st < steps; st++) {
+  // window scales of this lane's rows (byte 2 * phase + h: block g of half h of that stage)
+  uint32_t xwin[S::TX], wwin[S::TW];
+  const auto stage = [&](int st, auto phase) {
+    constexpr int PH = decltype(phase)::value;
     wait_loads_barrier<(S::D - 2) * S::LOADS>();
     issue(st + S::D - 1, buf == 0 ? S::D - 1 : buf - 1);
     const uint8_t* xs = smem + buf * S::STAGE + S::X0;
     const uint8_t* wl = smem + buf * S::STAGE + S::W0;
-    const uint8_t* sl = smem + buf * S::STAGE + S::S0;
-    if (S::MX) {
-      u32x4 xf[S::TX];
-      uint32_t xsc[S::TX];
+    // scale byte of block b of the stage (g of half h: 4h + g), row r of ROWS
+    const uint8_t* sl = S::SCALES == kWindows ? smem + S::WIN0 + (st / S::WS & 1) * S::WIN + st % S::WS * S::SB
+                                              : smem + buf * S::STAGE + S::S0;
+    const auto scale = [&](int r, int b) -> uint32_t {
+      if (S::SCALES == kWindows) return sl[r * 16 + b];
+      if (S::SCALES == kDwords) return sl[(b >> 2) * S::NH * S::T * 4 + r * 4 + (b & 3)];
+      return S::MX ? sl[(b >> 2) * S::NH * S::T * 4 + (r * 4 + (b & 3)) * 4] : sl[(r * 2 + b) * 4];
+    };
+    if constexpr (S::MX) {
+      if constexpr (S::SCALES == kWindows && PH == 0) {
 #pragma unroll
-      for (int x = 0; x < S::TX; x++) {
-        const int r = (wx * S::TX + x) * 16 + c;
-        xf[x] = *reinterpret_cast<const u32x4*>(xs + r * 64 + ((g ^ ((r >> 2) & 3)) << 4));
-        xsc[x] = S::BYTE_SCALES ? sl[((S::BN + r) * 4 + g) * 4] : sl[(S::BN + r) * 4 + g];
+        for (int x = 0; x < S::TX; x++) xwin[x] = window_bytes(sl, S::BN + (wx * S::TX + x) * 16 + c, g);
+#pragma unroll
+        for (int t = 0; t < S::TW; t++) wwin[t] = window_bytes(sl, w_local(t, c), g);
       }
+      const auto half = [&](auto hh) {
+        constexpr int H = decltype(hh)::value, SEL = S::SCALES == kWindows ? 2 * PH + H : 0;
+        u32x4 xf[S::TX];
+        uint32_t xsc[S::TX];
 #pragma unroll
-      for (int t = 0; t < S::TW; t++) {
-        const int r = w_local(t, c);
-        const u32x4 wf = *reinterpret_cast<const u32x4*>(wl + r * 64 + ((g ^ ((r / (4 * P)) & 3)) << 4));
-        const uint32_t s = S::BYTE_SCALES ? sl[(r * 4 + g) * 4] : sl[r * 4 + g];
+        for (int x = 0; x < S::TX; x++) {
+          const int r = (wx * S::TX + x) * 16 + c;
+          xf[x] = *reinterpret_cast<const u32x4*>(xs + r * 128 + (((4 * H + g) ^ ((r >> 1) & 7)) << 4));
+          xsc[x] = S::SCALES == kWindows ? xwin[x] : scale(S::BN + r, 4 * H + g);
+        }
 #pragma unroll
-        for (int x = 0; x < S::TX; x++) acc[t][x] = mfma_mx(wf, xf[x], acc[t][x], s, xsc[x]);
-      }
+        for (int t = 0; t < S::TW; t++) {
+          const int r = w_local(t, c);
+          const u32x4 wf = *reinterpret_cast<const u32x4*>(wl + r * 128 + (((4 * H + g) ^ w_swizzle(r)) << 4));
+          const uint32_t s = S::SCALES == kWindows ? wwin[t] : scale(r, 4 * H + g);
+#pragma unroll
+          for (int x = 0; x < S::TX; x++) acc[t][x] = mfma_mx<SEL, SEL>(wf, xf[x], acc[t][x], s, xsc[x]);
+        }
+      };
+      half(std::integral_constant<int, 0>());
+      half(std::integral_constant<int, 1>());
     } else {
       u32x4 xf[S::TX][2];
+      uint2 wf[S::TW];
+      uint32_t ws[S::TW];
 #pragma unroll
       for (int x = 0; x < S::TX; x++) {
         const int r = (wx * S::TX + x) * 16 + c;
@@ -234,9 +284,13 @@ void mx_tiled(MxArgs a, int gm, int vec) {
         const int r = w_local(t, c);
         // 16-row tile index in the order of the loads
         const int u = (r / (16 * P)) * P + (t % P);
-        const uint2 w = *reinterpret_cast<const uint2*>(wl + u * 512 + (((g >> 1) * 16 + c) << 4) + ((g & 1) << 3));
-        const float s = e8m0_operand(sl[(r * 2 + (g >> 1)) * 4]);
-        const u32x4 w0 = mx_decode8(w.x, s), w1 = mx_decode8(w.y, s);
+        wf[t] = *reinterpret_cast<const uint2*>(wl + u * 512 + (((g >> 1) * 16 + c) << 4) + ((g & 1) << 3));
+        ws[t] = scale(r, g >> 1);
+      }
+#pragma unroll
+      for (int t = 0; t < S::TW; t++) {
+        const float s = e8m0_operand(ws[t]);
+        const u32x4 w0 = mx_decode8(wf[t].x, s), w1 = mx_decode8(wf[t].y, s);
 #pragma unroll
         for (int x = 0; x < S::TX; x++) acc[t][x] = mfma16(w0, xf[x][0], acc[t][x]);
 #pragma unroll
@@ -244,6 +298,14 @@ void mx_tiled(MxArgs a, int gm, int vec) {
       }
     }
     buf = buf + 1 == S::D ? 0 : buf + 1;
+  };
+  if constexpr (S::MX && S::SCALES == kWindows) {
+    for (int st = 0; st < steps; st += 2) {  // K is whole windows
+      stage(st, std::integral_constant<int, 0>());
+      stage(st + 1, std::integral_constant<int, 1>());
+    }
+  } else {
+    for (int st = 0; st < steps; st++) stage(st, std::integral_constant<int, 0>());
   }
   wait_loads<0>();  // nothing writes LDS after the workgroup
 
@@ -337,14 +399,15 @@ hipError_t launch_shape(const MxArgs& a, hipStream_t stream) {
   const int64_t nbm = a.tiles ? a.max_tiles : (a.M + S::BM - 1) / S::BM;
   const int64_t groups = nbm * ((cols + bc - 1) / bc);
   if (groups * S::T > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
-  const int gm = S::MX ? 4 : 2;
+  // an XCD's 32 CUs work on gm x (32 / gm) tiles (grouped: on the columns of a few list tiles)
+  const int gm = a.tiles ? 1 : S::MX ? 4 : 2;
   const int64_t ysz = a.y_type == MXFP4_F32 ? 4 : 2, ld = a.swiglu ? cols : a.ldy;
   const int vec = ((uintptr_t)a.y | (uintptr_t)(ld * ysz)) % 16 == 0;
   auto k = !a.tiles ? mx_tiled<S, false, 0>
            : a.swiglu == 0 ? mx_tiled<S, true, 0>
            : a.swiglu == MXFP4_OUT_SWIGLU_BF16 ? mx_tiled<S, true, MXFP4_OUT_SWIGLU_BF16>
                                                : mx_tiled<S, true, MXFP4_OUT_SWIGLU_MXFP4>;
-  hipLaunchKernelGGL(k, dim3((uint32_t)groups), dim3(S::T), S::LDS, stream, a, a.tiles ? 1 : gm, vec);
+  hipLaunchKernelGGL(k, dim3((uint32_t)groups), dim3(S::T), S::LDS, stream, a, gm, vec);
   return hipGetLastError();
 }
 
@@ -352,17 +415,21 @@ constexpr int64_t kFewTiles = 200;
 
 //LAUNCH
 template <int ACT, int BM, int BN, int WX, int WW, int D>
-hipError_t launch_scales(const MxArgs& a, bool dwords, hipStream_t stream) {
-  if constexpr (ACT == MXFP4_ACT_MXFP4) {
-    if (!dwords) return launch_shape<Shape<ACT, BM, BN, WX, WW, (D > 3 ? D - 1 : D), true>>(a, stream);
+hipError_t launch_scales(const MxArgs& a, hipStream_t stream) {
+  constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
+  const uintptr_t at = (uintptr_t)a.w_scales | (MX ? (uintptr_t)a.x_scales : 0);
+  if (a.K % 512 == 0 && at % 16 == 0)
+    return launch_shape<Shape<ACT, BM, BN, WX, WW, D, kWindows>>(a, stream);
+  if constexpr (MX) {
+    if (a.K % 128 == 0 && at % 4 == 0) return launch_shape<Shape<ACT, BM, BN, WX, WW, D, kDwords>>(a, stream);
   }
-  return launch_shape<Shape<ACT, BM, BN, WX, WW, D, false>>(a, stream);
+  // (two stages of the largest MXFP4 tile do not fit with byte scales)
+  return launch_shape<Shape<ACT, (MX && BM * BN == 256 * 256 ? 128 : BM), BN, WX, WW, D, kBytes>>(a, stream);
 }
 
 template <int ACT>
 hipError_t launch_act(const MxArgs& a, hipStream_t stream) {
   constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
-  const bool dwords = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.w_scales) % 4 == 0;
   const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
   // workgroups that tiles of bm rows and bn weight rows make
   const auto tiles = [&](int64_t bm, int64_t bn) {
@@ -370,10 +437,10 @@ hipError_t launch_act(const MxArgs& a, hipStream_t stream) {
     return (a.tiles ? a.max_tiles : (a.M + bm - 1) / bm) * ((cols + bc - 1) / bc);
   };
   const int64_t rows = a.tiles ? a.tile_rows : a.M;
-  if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_scales<ACT, 256, 256, MX ? 2 : 4, MX ? 4 : 2, MX ? 4 : 3>(a, dwords, stream);
-  if (rows > 64 && tiles(128, 256) >= kFewTiles) return launch_scales<ACT, 128, 256, MX ? 2 : 4, MX ? 4 : 2, 4>(a, dwords, stream);
-  if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_scales<ACT, 128, 128, 2, 2, 4>(a, dwords, stream);
-  return launch_scales<ACT, 64, 128, 2, 2, 4>(a, dwords, stream);
+  if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_scales<ACT, 256, 256, MX ? 2 : 4, MX ? 4 : 2, MX ? 2 : 3>(a, stream);
+  if (rows > 64 && tiles(128, 256) >= kFewTiles) return launch_scales<ACT, 128, 256, MX ? 2 : 4, MX ? 4 : 2, MX ? 2 : 4>(a, stream);
+  if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_scales<ACT, 128, 128, 2, 2, MX ? 3 : 4>(a, stream);
+  return launch_scales<ACT, 64, 128, 2, 2, MX ? 3 : 4>(a, stream);
 }
 //END
 
