@@ -53,6 +53,7 @@ struct Shape {
   static constexpr int WIN0 = D * STAGE, WIN = SCALES == kWindows ? NS * T * 16 : 0;  // two windows
   static constexpr int SINK = WIN0 + 2 * WIN;  // where loads go whose bytes nobody reads
   static constexpr int LDS = SINK + 1024;
+  static_assert(16 * TW * 16 * 4 * WX * WW <= LDS, "the results' way out");
   static_assert(SCALES != kWindows || D <= WS + 1, "a window is overwritten two windows later");
   static_assert(SCALES != kDwords || MX, "");
   static_assert(NX * 16 * T == BM * XB && NW * 16 * T == BN * WB, "whole loads only");
@@ -66,6 +67,52 @@ __device__ __forceinline__ uint32_t window_bytes(const uint8_t* win, int r, int 
   const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], 0x0400u + 0x0101u * (uint32_t)g);
   const uint32_t hi = __builtin_amdgcn_perm(v[3], v[2], 0x0400u + 0x0101u * (uint32_t)g);
   return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
+// LDS that store_tile takes of each wave: a row tile of fp32
+template <class S>
+__host__ __device__ constexpr int store_bytes() {
+  return 16 * S::TW * 16 * 4;
+}
+
+// A wave's results to rows of y, for whole columns and 16-byte aligned rows. In registers, 16
+// consecutive lanes hold 16 rows, so a store from there would touch 64 cache lines; each
+// tile of 16 rows goes through LDS and out as whole lines, ES bytes a value. Piece q of row r
+// lies at slot q ^ f(r), as in the operands' tiles.
+template <class S, bool GROUPED, int ES>
+__device__ __forceinline__ void store_tile(const MxArgs& a, uint8_t* lds, f32x4 (&acc)[S::TW][S::TX],
+                                           int wx, int64_t m0, int slot0, int64_t rows_m, int64_t n) {
+  constexpr int RB = S::TW * 16 * ES, PIECES = RB / 16, ROWS = 64 / PIECES;  // rows of a store
+  static_assert(PIECES >= 8 && PIECES <= 64, "");
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const auto swizzle = [](int r) { return PIECES == 8 ? (r >> 1) & 7 : r & 15; };
+#pragma unroll
+  for (int x = 0; x < S::TX; x++) {
+    const int r0 = (wx * S::TX + x) * 16;
+    if (r0 >= rows_m) break;
+    const int route = GROUPED && r0 + c < rows_m ? a.sorted[slot0 + r0 + c] : 0;
+#pragma unroll
+    for (int w = 0; w < S::TW; w += ES == 4 ? 1 : 2) {  // one 16-byte piece
+      // tiles w .. of group w / 4 hold columns 64 * (w / 4) + 16 * g + 4 * (w % 4) and on
+      const int piece = (64 * (w / 4) + 16 * g + 4 * (w % 4)) * ES / 16;
+      u32x4 v;
+      if constexpr (ES == 4) {
+        v = __builtin_bit_cast(u32x4, acc[w][x]);
+      } else {
+        const f32x4 p = acc[w][x], q = acc[w + 1][x];
+        v = u32x4{bf16_pair(p[0], p[1]), bf16_pair(p[2], p[3]), bf16_pair(q[0], q[1]), bf16_pair(q[2], q[3])};
+      }
+      *reinterpret_cast<u32x4*>(lds + c * RB + ((piece ^ swizzle(c)) << 4)) = v;
+    }
+#pragma unroll
+    for (int i = 0; i < 16 / ROWS; i++) {
+      const int r = i * ROWS + lane / PIECES, q = lane % PIECES;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * RB + ((q ^ swizzle(r)) << 4));
+      const int64_t row = GROUPED ? __shfl(route, r, 64) : m0 + r0 + r;
+      if (r0 + r < rows_m)
+        *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.y) + (row * a.ldy + n) * ES + 16 * q) = v;
+    }
+  }
 }
 
 template <class S, bool GROUPED, int SWIGLU>
@@ -309,6 +356,16 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   }
   wait_loads<0>();  // nothing writes LDS after the workgroup
 
+  if constexpr (!SWIGLU) {
+    if (vec && n0 + S::BN <= N) {
+      wait_loads_barrier<0>();  // the other waves have read their last stage
+      if (a.y_type == MXFP4_F32)
+        store_tile<S, GROUPED, 4>(a, smem + wave * store_bytes<S>(), acc, wx, m0, slot0, rows_m, n0 + ww * S::TW * 16);
+      else
+        store_tile<S, GROUPED, 2>(a, smem + wave * store_bytes<S>(), acc, wx, m0, slot0, rows_m, n0 + ww * S::TW * 16);
+      return;
+    }
+  }
 #pragma unroll
   for (int x = 0; x < S::TX; x++) {
     const int r = (wx * S::TX + x) * 16 + c;
