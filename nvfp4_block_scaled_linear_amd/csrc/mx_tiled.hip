@@ -12,7 +12,8 @@
 //    sides), 64 k for BF16 ones (128 bytes of activations, 32 of codes).
 //  - LDS rows have no padding (the loads write 1 KiB runs); 16-byte piece q of a row lies at
 //    slot q ^ f(row), with f such that the 16 rows that lanes read together fall into
-//    different banks.
+//    different banks. (A 16-byte read takes lanes of two neighbouring g together, whose pieces
+//    have to differ in the lowest bit: piece 2g + j of BF16 rows counts as g + 4j.)
 //  - Weight row 4P * a + 4s + b of a group of 16P rows is row 4a + b of the MFMA of its s-th
 //    16-row tile (P tiles to a group): a lane's results are then 4P consecutive columns, so
 //    it stores 16 bytes at a time and holds a block's half or quarter when SwiGLU's result is
@@ -189,7 +190,8 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   for (int i = 0; i < S::NX; i++) {
     const int p = i * S::T + tid;
     const int r = p >> 3;
-    const int q = (p & 7) ^ ((r >> 1) & 7);
+    int q = (p & 7) ^ ((r >> 1) & 7);
+    if (!S::MX) q = (q & 3) << 1 | q >> 2;
     xk[i] = q;
     xo[i] = r < rows_m ? (uint32_t)(x_row(r) * xpitch) + 16 * q : kOutOfRange;
   }
@@ -211,8 +213,9 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   }
   const u32x4 wsr = lds_load_rsrc(ws + (SWIGLU ? 0 : n0 * nb), (N - (SWIGLU ? 0 : n0)) * nb);
   const u32x4 xsr = S::MX ? lds_load_rsrc(a.x_scales + (GROUPED ? 0 : m0 * nb), x_last * nb) : wsr;
-  // scale loads: the p-th is block p % PER (a dword: all four; a window: all sixteen) of row p /
-  // PER, of the weight, then of the activations. Whole waves read one side (BN is a multiple
+  // scale loads: the p-th is block p % PER (a dword: all four; a window: all sixteen) of the p /
+  // PER-th row, of the weight, then of the activations; the weight's rows in the order in which
+  // lanes read them, 16 side by side. Whole waves read one side (BN is a multiple
   // of 64), so the descriptor is uniform.
   bool s_is_x[S::NS];
 #pragma unroll
@@ -221,7 +224,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     sk[i] = p % S::PER + i / S::NH * 4;
     s_is_x[i] = S::MX && __builtin_amdgcn_readfirstlane(t) >= S::BN;
     int64_t row = -1;
-    if (t < S::BN) row = w_row(t);
+    if (t < S::BN) row = w_row(t / (16 * P) * (16 * P) + 4 * P * ((t & 15) >> 2) + 4 * ((t >> 4) % P) + (t & 3));
     else if (S::MX && t - S::BN < rows_m) row = x_row(t - S::BN);
     so[i] = row >= 0 ? (uint32_t)(row * nb) + sk[i] : kOutOfRange;
   }
@@ -260,26 +263,24 @@ void mx_tiled(MxArgs a, int gm, int vec) {
 #pragma unroll
     for (int x = 0; x < S::TX; x++) acc[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // tile row of MFMA row 4a + b of this wave's weight tile t
-  const auto w_local = [&](int t, int row) {
-    const int grp = t / P, s = t % P;
-    const int base = SWIGLU ? grp * BC + ww * 16 * P : (ww * GROUPS + grp) * 16 * P;
-    return base + 4 * P * (row >> 2) + 4 * s + (row & 3);
-  };
+  // first tile row of the group of this wave's weight tile t; tile row of the tile's MFMA row
+  // 4a + b; and where that row's scales are
+  const auto w_group = [&](int t) { return SWIGLU ? t / P * BC + ww * 16 * P : (ww * GROUPS + t / P) * 16 * P; };
+  const auto w_local = [&](int t, int row) { return w_group(t) + 4 * P * (row >> 2) + 4 * (t % P) + (row & 3); };
+  const auto w_scale = [&](int t, int row) { return w_group(t) + 16 * (t % P) + row; };
 
   const int steps = (nblk + S::SB - 1) / S::SB;
 #pragma unroll
   for (int i = 0; i < S::D - 1; i++) issue(i, i);
-  int buf = 0;
   // window scales of this lane's rows (byte 2 * phase + h: block g of half h of that stage)
   uint32_t xwin[S::TX], wwin[S::TW];
-  const auto stage = [&](int st, auto phase) {
+  const auto stage = [&](int st, auto phase, int buf) {
     constexpr int PH = decltype(phase)::value;
     wait_loads_barrier<(S::D - 2) * S::LOADS>();
     issue(st + S::D - 1, buf == 0 ? S::D - 1 : buf - 1);
     const uint8_t* xs = smem + buf * S::STAGE + S::X0;
     const uint8_t* wl = smem + buf * S::STAGE + S::W0;
-    // scale byte of block b of the stage (g of half h: 4h + g), row r of ROWS
+    // scale byte of block b of the stage (g of half h: 4h + g), r-th of ROWS
     const uint8_t* sl = S::SCALES == kWindows ? smem + S::WIN0 + (st / S::WS & 1) * S::WIN + st % S::WS * S::SB
                                               : smem + buf * S::STAGE + S::S0;
     const auto scale = [&](int r, int b) -> uint32_t {
@@ -292,7 +293,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
 #pragma unroll
         for (int x = 0; x < S::TX; x++) xwin[x] = window_bytes(sl, S::BN + (wx * S::TX + x) * 16 + c, g);
 #pragma unroll
-        for (int t = 0; t < S::TW; t++) wwin[t] = window_bytes(sl, w_local(t, c), g);
+        for (int t = 0; t < S::TW; t++) wwin[t] = window_bytes(sl, w_scale(t, c), g);
       }
       const auto half = [&](auto hh) {
         constexpr int H = decltype(hh)::value, SEL = S::SCALES == kWindows ? 2 * PH + H : 0;
@@ -308,7 +309,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
         for (int t = 0; t < S::TW; t++) {
           const int r = w_local(t, c);
           const u32x4 wf = *reinterpret_cast<const u32x4*>(wl + r * 128 + (((4 * H + g) ^ w_swizzle(r)) << 4));
-          const uint32_t s = S::SCALES == kWindows ? wwin[t] : scale(r, 4 * H + g);
+          const uint32_t s = S::SCALES == kWindows ? wwin[t] : scale(w_scale(t, c), 4 * H + g);
 #pragma unroll
           for (int x = 0; x < S::TX; x++) acc[t][x] = mfma_mx<SEL, SEL>(wf, xf[x], acc[t][x], s, xsc[x]);
         }
@@ -324,7 +325,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
         const int r = (wx * S::TX + x) * 16 + c;
 #pragma unroll
         for (int j = 0; j < 2; j++)
-          xf[x][j] = *reinterpret_cast<const u32x4*>(xs + r * 128 + (((2 * g + j) ^ ((r >> 1) & 7)) << 4));
+          xf[x][j] = *reinterpret_cast<const u32x4*>(xs + r * 128 + (((g + 4 * j) ^ ((r >> 1) & 7)) << 4));
       }
 #pragma unroll
       for (int t = 0; t < S::TW; t++) {
@@ -332,7 +333,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
         // 16-row tile index in the order of the loads
         const int u = (r / (16 * P)) * P + (t % P);
         wf[t] = *reinterpret_cast<const uint2*>(wl + u * 512 + (((g >> 1) * 16 + c) << 4) + ((g & 1) << 3));
-        ws[t] = scale(r, g >> 1);
+        ws[t] = scale(w_scale(t, c), g >> 1);
       }
 #pragma unroll
       for (int t = 0; t < S::TW; t++) {
@@ -344,15 +345,19 @@ void mx_tiled(MxArgs a, int gm, int vec) {
         for (int x = 0; x < S::TX; x++) acc[t][x] = mfma16(w1, xf[x][1], acc[t][x]);
       }
     }
-    buf = buf + 1 == S::D ? 0 : buf + 1;
   };
-  if constexpr (S::MX && S::SCALES == kWindows) {
-    for (int st = 0; st < steps; st += 2) {  // K is whole windows
-      stage(st, std::integral_constant<int, 0>());
-      stage(st + 1, std::integral_constant<int, 1>());
+  // the ring's buffers are taken in turn, by loops that are unrolled so that they are constants
+  constexpr bool PAIRS = S::MX && S::SCALES == kWindows;  // K is whole windows of two stages
+  constexpr int UNROLL = PAIRS && S::D % 2 ? 2 * S::D : S::D;
+  for (int st0 = 0; st0 < steps; st0 += UNROLL) {
+#pragma unroll
+    for (int i = 0; i < UNROLL; i++) {
+      if (i && st0 + i >= steps) break;
+      if (PAIRS && i % 2)
+        stage(st0 + i, std::integral_constant<int, PAIRS>(), i % S::D);
+      else
+        stage(st0 + i, std::integral_constant<int, 0>(), i % S::D);
     }
-  } else {
-    for (int st = 0; st < steps; st++) stage(st, std::integral_constant<int, 0>());
   }
   wait_loads<0>();  // nothing writes LDS after the workgroup
 
