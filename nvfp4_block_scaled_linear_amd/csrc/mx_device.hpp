@@ -97,6 +97,7 @@ __device__ __forceinline__ u32x4 lds_load_rsrc(const void* base, int64_t bytes) 
 template <int BYTES>
 __device__ __forceinline__ void lds_load(u32x4 rsrc, uint32_t off, uint32_t lds) {
   static_assert(BYTES == 16 || BYTES == 4 || BYTES == 1, "");
+  lds = __builtin_amdgcn_readfirstlane(lds);
   if (BYTES == 16)
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :: "v"(off), "s"(rsrc), "s"(lds) : "memory");

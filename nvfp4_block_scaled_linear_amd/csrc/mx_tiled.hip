@@ -27,36 +27,29 @@
 namespace nvfp4 {
 namespace {
 
-// How the scales are loaded. A load costs by the cache lines it looks up, and every row is one,
-// so windows of 16 bytes a row (512 k) are taken where rows are aligned to them; otherwise a
-// dword a row for 128 k (MXFP4 activations), or a byte per row and block.
-enum Scales { kBytes, kDwords, kWindows };
-
-template <int ACT_, int BM_, int BN_, int WX_, int WW_, int D_, int SCALES_>
+// SHIFT: scale rows that are not dword-aligned, or K that ends inside a stage.
+template <int ACT_, int BM_, int BN_, int WX_, int WW_, int D_, bool SHIFT_>
 struct Shape {
-  static constexpr int ACT = ACT_, BM = BM_, BN = BN_, WX = WX_, WW = WW_, D = D_, SCALES = SCALES_;
+  static constexpr int ACT = ACT_, BM = BM_, BN = BN_, WX = WX_, WW = WW_, D = D_;
+  static constexpr bool SHIFT = SHIFT_;
   static constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
   static constexpr int T = 64 * WX * WW;
   static constexpr int TX = BM / WX / 16, TW = BN / WW / 16;
   static constexpr int XB = 128, WB = MX ? 128 : 32;  // bytes of a row per stage
   static constexpr int SB = MX ? 8 : 2;               // weight blocks per stage
   static constexpr int NX = BM * XB / (16 * T), NW = BN * WB / (16 * T);
-  // rows with scales: the weight's, and MXFP4 activations'. Scale loads of a stage: windows,
-  // one load in WS stages (in the others it is out of range); otherwise for each 128 k half of
-  // MXFP4 activations' stage, or for the stage
-  static constexpr int ROWS = MX ? BM + BN : BN, WS = MX ? 2 : 8;
-  static constexpr int PER = SCALES == kBytes ? (MX ? 4 : 2) : 1;  // loads of a row and half
-  static constexpr int NH = (ROWS * PER + T - 1) / T;
-  static constexpr int NS = MX && SCALES != kWindows ? 2 * NH : NH;
+  // Scales come in windows of 16 bytes a row, WS stages of them at a time (a load costs by the
+  // cache lines it looks up, and every row is one), one load in WS stages and out of range in
+  // the others. A SHIFT window begins up to three bytes before its first scale, at a dword.
+  static constexpr int ROWS = MX ? BM + BN : BN, NS = (ROWS + T - 1) / T;
+  static constexpr int WS = MX ? (SHIFT ? 1 : 2) : (SHIFT ? 6 : 8);
   static constexpr int LOADS = NX + NW + NS;
-  static constexpr int X0 = 0, W0 = BM * XB, S0 = W0 + BN * WB;
-  static constexpr int STAGE = S0 + (SCALES == kWindows ? 0 : NS * T * 4);
-  static constexpr int WIN0 = D * STAGE, WIN = SCALES == kWindows ? NS * T * 16 : 0;  // two windows
-  static constexpr int SINK = WIN0 + 2 * WIN;  // where loads go whose bytes nobody reads
+  static constexpr int X0 = 0, W0 = BM * XB, STAGE = W0 + BN * WB;
+  static constexpr int WIN = NS * T * 16, WINDOWS = WS == 1 ? D : 2;
+  static constexpr int WIN0 = D * STAGE, SINK = WIN0 + WINDOWS * WIN;  // SINK: bytes that nobody reads
   static constexpr int LDS = SINK + 1024;
+  static_assert(SB * WS + 3 * SHIFT <= 16 && (WINDOWS - 1) * WS >= D - 1, "a window is in use until it is overwritten");
   static_assert(16 * TW * 16 * 4 * WX * WW <= LDS, "the results' way out");
-  static_assert(SCALES != kWindows || D <= WS + 1, "a window is overwritten two windows later");
-  static_assert(SCALES != kDwords || MX, "");
   static_assert(NX * 16 * T == BM * XB && NW * 16 * T == BN * WB, "whole loads only");
   static_assert(LDS <= 160 * 1024, "LDS");
   static_assert(TW % 4 == 0, "weight rows come in groups of 64 (SwiGLU: 32 + 32)");
@@ -76,17 +69,20 @@ __host__ __device__ constexpr int store_bytes() {
   return 16 * S::TW * 16 * 4;
 }
 
-// A wave's results to rows of y, for whole columns and 16-byte aligned rows. In registers, 16
-// consecutive lanes hold 16 rows, so a store from there would touch 64 cache lines; each
-// tile of 16 rows goes through LDS and out as whole lines, ES bytes a value. Piece q of row r
-// lies at slot q ^ f(r), as in the operands' tiles.
+// A wave's results to rows of y, ES bytes a value; cols columns are left from n on. In
+// registers, 16 consecutive lanes hold 16 rows, so a store from there would touch 64 cache
+// lines; each tile of 16 rows goes through LDS and out along the rows, 16 bytes a lane, or a
+// value a lane where rows are not aligned or end inside (1001 columns of fp32 stored from
+// registers took 10 of 20 us). Piece q of row r lies at slot q ^ f(r), as in the operands.
 template <class S, bool GROUPED, int ES>
 __device__ __forceinline__ void store_tile(const MxArgs& a, uint8_t* lds, f32x4 (&acc)[S::TW][S::TX],
-                                           int wx, int64_t m0, int slot0, int64_t rows_m, int64_t n) {
+                                           int wx, int64_t m0, int slot0, int64_t rows_m, int64_t n,
+                                           int64_t cols, bool vec) {
   constexpr int RB = S::TW * 16 * ES, PIECES = RB / 16, ROWS = 64 / PIECES;  // rows of a store
   static_assert(PIECES >= 8 && PIECES <= 64, "");
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const auto swizzle = [](int r) { return PIECES == 8 ? (r >> 1) & 7 : r & 15; };
+  const bool whole = vec && cols >= S::TW * 16;
 #pragma unroll
   for (int x = 0; x < S::TX; x++) {
     const int r0 = (wx * S::TX + x) * 16;
@@ -105,13 +101,29 @@ __device__ __forceinline__ void store_tile(const MxArgs& a, uint8_t* lds, f32x4 
       }
       *reinterpret_cast<u32x4*>(lds + c * RB + ((piece ^ swizzle(c)) << 4)) = v;
     }
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < 16 / ROWS; i++) {
-      const int r = i * ROWS + lane / PIECES, q = lane % PIECES;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * RB + ((q ^ swizzle(r)) << 4));
-      const int64_t row = GROUPED ? __shfl(route, r, 64) : m0 + r0 + r;
-      if (r0 + r < rows_m)
-        *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.y) + (row * a.ldy + n) * ES + 16 * q) = v;
+      for (int i = 0; i < 16 / ROWS; i++) {
+        const int r = i * ROWS + lane / PIECES, q = lane % PIECES;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * RB + ((q ^ swizzle(r)) << 4));
+        const int64_t row = GROUPED ? __shfl(route, r, 64) : m0 + r0 + r;
+        if (r0 + r < rows_m)
+          *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.y) + (row * a.ldy + n) * ES + 16 * q) = v;
+      }
+      continue;
+    }
+    for (int r = 0; r < 16 && r0 + r < rows_m; r++) {
+      const int64_t row = GROUPED ? __builtin_amdgcn_readlane(route, r) : m0 + r0 + r;
+#pragma unroll
+      for (int k = 0; k < S::TW / 4; k++) {
+        const int e = 64 * k + lane;  // column of the wave's
+        const uint8_t* p = lds + r * RB + (((e * ES >> 4) ^ swizzle(r)) << 4) + (e * ES & 15);
+        if (e >= cols) continue;
+        if constexpr (ES == 4)
+          static_cast<uint32_t*>(a.y)[row * a.ldy + n + e] = *reinterpret_cast<const uint32_t*>(p);
+        else
+          static_cast<uint16_t*>(a.y)[row * a.ldy + n + e] = *reinterpret_cast<const uint16_t*>(p);
+      }
     }
   }
 }
@@ -184,8 +196,8 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   const auto w_swizzle = [](int t) { return ((t >> 1) & 1) | ((t / (4 * P)) & 3) << 1; };
 
   // this lane's loads of stage 0; a stage on, offsets grow by XB / WB / SB bytes
-  uint32_t xo[S::NX], wo[S::NW], so[S::NS];
-  int xk[S::NX], wk[S::NW], sk[S::NS];  // first block (BF16 x: first 8-value piece) of the load
+  uint32_t xo[S::NX], wo[S::NW];
+  int xk[S::NX], wk[S::NW];  // first block (BF16 x: first 8-value piece) of the load
 #pragma unroll
   for (int i = 0; i < S::NX; i++) {
     const int p = i * S::T + tid;
@@ -211,23 +223,30 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     const int64_t row = w_row(t);
     wo[i] = row >= 0 ? (uint32_t)(row * (K >> 1)) + 16 * q : kOutOfRange;
   }
-  const u32x4 wsr = lds_load_rsrc(ws + (SWIGLU ? 0 : n0 * nb), (N - (SWIGLU ? 0 : n0)) * nb);
-  const u32x4 xsr = S::MX ? lds_load_rsrc(a.x_scales + (GROUPED ? 0 : m0 * nb), x_last * nb) : wsr;
-  // scale loads: the p-th is block p % PER (a dword: all four; a window: all sixteen) of the p /
-  // PER-th row, of the weight, then of the activations; the weight's rows in the order in which
-  // lanes read them, 16 side by side. Whole waves read one side (BN is a multiple
-  // of 64), so the descriptor is uniform.
+  // Scales of one side: rows of nb bytes from p, counted from the dword that p lies in.
+  const auto scales_of = [](const uint8_t* p, int64_t bytes) {
+    const int64_t skip = (uintptr_t)p & 3;
+    return lds_load_rsrc(p - skip, (skip + bytes + 3) & ~(int64_t)3);
+  };
+  const uint8_t* wsp = ws + (SWIGLU ? 0 : n0 * nb);
+  const uint8_t* xsp = S::MX ? a.x_scales + (GROUPED ? 0 : m0 * nb) : wsp;
+  const u32x4 wsr = scales_of(wsp, (N - (SWIGLU ? 0 : n0)) * nb);
+  const u32x4 xsr = S::MX ? scales_of(xsp, x_last * nb) : wsr;
+  // the p-th scale load is that of the p-th row, of the weight, then of the activations; the
+  // weight's rows in the order in which lanes read them, 16 side by side. Whole waves read one
+  // side (BN is a multiple of 64), so the descriptor is uniform.
   bool s_is_x[S::NS];
+  uint32_t so[S::NS];
 #pragma unroll
   for (int i = 0; i < S::NS; i++) {
-    const int p = (i % S::NH) * S::T + tid, t = p / S::PER;
-    sk[i] = p % S::PER + i / S::NH * 4;
+    const int t = i * S::T + tid;
     s_is_x[i] = S::MX && __builtin_amdgcn_readfirstlane(t) >= S::BN;
     int64_t row = -1;
     if (t < S::BN) row = w_row(t / (16 * P) * (16 * P) + 4 * P * ((t & 15) >> 2) + 4 * ((t >> 4) % P) + (t & 3));
     else if (S::MX && t - S::BN < rows_m) row = x_row(t - S::BN);
-    so[i] = row >= 0 ? (uint32_t)(row * nb) + sk[i] : kOutOfRange;
+    so[i] = row >= 0 ? ((uint32_t)(row * nb) + (uint32_t)((uintptr_t)(s_is_x[i] ? xsp : wsp) & 3)) & ~3u : kOutOfRange;
   }
+
   const uint32_t lds0 = lds_address(smem);
   const int nblk = (int)nb;
   const auto issue = [&](int st, int buf) {
@@ -244,16 +263,10 @@ void mx_tiled(MxArgs a, int gm, int vec) {
                    base + S::W0 + (i * S::T + wave * 64) * 16);
 #pragma unroll
     for (int i = 0; i < S::NS; i++) {
-      const u32x4 sr = s_is_x[i] ? xsr : wsr;
-      if (S::SCALES == kWindows) {
-        const int w = st / S::WS;
-        const bool now = st % S::WS == 0 && S::SB * st < nblk;
-        lds_load<16>(sr, now ? so[i] + 16 * w : kOutOfRange,
-                     now ? lds0 + S::WIN0 + (w & 1) * S::WIN + (i * S::T + wave * 64) * 16 : lds0 + S::SINK);
-      } else {
-        const uint32_t off = S::SB * st + sk[i] < nblk ? so[i] + st * S::SB : kOutOfRange;
-        lds_load<S::SCALES == kDwords ? 4 : 1>(sr, off, base + S::S0 + (i * S::T + wave * 64) * 4);
-      }
+      const int w = st / S::WS;
+      const bool now = st % S::WS == 0 && S::SB * st < nblk;
+      lds_load<16>(s_is_x[i] ? xsr : wsr, now ? so[i] + S::SB * S::WS * w : kOutOfRange,
+                   now ? lds0 + S::WIN0 + w % S::WINDOWS * S::WIN + (i * S::T + wave * 64) * 16 : lds0 + S::SINK);
     }
   };
 
@@ -269,6 +282,24 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   const auto w_local = [&](int t, int row) { return w_group(t) + 4 * P * (row >> 2) + 4 * (t % P) + (row & 3); };
   const auto w_scale = [&](int t, int row) { return w_group(t) + 16 * (t % P) + row; };
 
+  // SHIFT: where in its dword the first scale of this lane's rows lies, two bits a tile
+  uint32_t w_shift = 0u, x_shift = 0u;
+  if (S::SHIFT) {
+#pragma unroll
+    for (int t = 0; t < S::TW; t++) {
+      const int64_t row = w_row(w_local(t, c));
+      w_shift |= (((uint32_t)row * (uint32_t)nb + (uint32_t)(uintptr_t)wsp) & 3u) << (2 * t);
+    }
+    if (S::MX) {
+#pragma unroll
+      for (int x = 0; x < S::TX; x++) {
+        const int r = (wx * S::TX + x) * 16 + c;
+        const int64_t row = r < rows_m ? x_row(r) : 0;
+        x_shift |= (((uint32_t)row * (uint32_t)nb + (uint32_t)(uintptr_t)xsp) & 3u) << (2 * x);
+      }
+    }
+  }
+
   const int steps = (nblk + S::SB - 1) / S::SB;
 #pragma unroll
   for (int i = 0; i < S::D - 1; i++) issue(i, i);
@@ -280,36 +311,34 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     issue(st + S::D - 1, buf == 0 ? S::D - 1 : buf - 1);
     const uint8_t* xs = smem + buf * S::STAGE + S::X0;
     const uint8_t* wl = smem + buf * S::STAGE + S::W0;
-    // scale byte of block b of the stage (g of half h: 4h + g), r-th of ROWS
-    const uint8_t* sl = S::SCALES == kWindows ? smem + S::WIN0 + (st / S::WS & 1) * S::WIN + st % S::WS * S::SB
-                                              : smem + buf * S::STAGE + S::S0;
-    const auto scale = [&](int r, int b) -> uint32_t {
-      if (S::SCALES == kWindows) return sl[r * 16 + b];
-      if (S::SCALES == kDwords) return sl[(b >> 2) * S::NH * S::T * 4 + r * 4 + (b & 3)];
-      return S::MX ? sl[(b >> 2) * S::NH * S::T * 4 + (r * 4 + (b & 3)) * 4] : sl[(r * 2 + b) * 4];
+    // scale byte of block b of the stage (g of half h: 4h + g), r-th of ROWS, shifted by sh
+    const uint8_t* sl = smem + S::WIN0 + st / S::WS % S::WINDOWS * S::WIN + st % S::WS * S::SB;
+    const auto scale = [&](int r, int b, uint32_t sh) -> uint32_t {
+      if (!S::SHIFT) return sl[r * 16 + b];
+      return S::SB * st + b < nblk ? sl[r * 16 + b + sh] : 0u;
     };
     if constexpr (S::MX) {
-      if constexpr (S::SCALES == kWindows && PH == 0) {
+      if constexpr (!S::SHIFT && PH == 0) {
 #pragma unroll
         for (int x = 0; x < S::TX; x++) xwin[x] = window_bytes(sl, S::BN + (wx * S::TX + x) * 16 + c, g);
 #pragma unroll
         for (int t = 0; t < S::TW; t++) wwin[t] = window_bytes(sl, w_scale(t, c), g);
       }
       const auto half = [&](auto hh) {
-        constexpr int H = decltype(hh)::value, SEL = S::SCALES == kWindows ? 2 * PH + H : 0;
+        constexpr int H = decltype(hh)::value, SEL = !S::SHIFT ? 2 * PH + H : 0;
         u32x4 xf[S::TX];
         uint32_t xsc[S::TX];
 #pragma unroll
         for (int x = 0; x < S::TX; x++) {
           const int r = (wx * S::TX + x) * 16 + c;
           xf[x] = *reinterpret_cast<const u32x4*>(xs + r * 128 + (((4 * H + g) ^ ((r >> 1) & 7)) << 4));
-          xsc[x] = S::SCALES == kWindows ? xwin[x] : scale(S::BN + r, 4 * H + g);
+          xsc[x] = !S::SHIFT ? xwin[x] : scale(S::BN + r, 4 * H + g, x_shift >> (2 * x) & 3);
         }
 #pragma unroll
         for (int t = 0; t < S::TW; t++) {
           const int r = w_local(t, c);
           const u32x4 wf = *reinterpret_cast<const u32x4*>(wl + r * 128 + (((4 * H + g) ^ w_swizzle(r)) << 4));
-          const uint32_t s = S::SCALES == kWindows ? wwin[t] : scale(w_scale(t, c), 4 * H + g);
+          const uint32_t s = !S::SHIFT ? wwin[t] : scale(w_scale(t, c), 4 * H + g, w_shift >> (2 * t) & 3);
 #pragma unroll
           for (int x = 0; x < S::TX; x++) acc[t][x] = mfma_mx<SEL, SEL>(wf, xf[x], acc[t][x], s, xsc[x]);
         }
@@ -333,7 +362,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
         // 16-row tile index in the order of the loads
         const int u = (r / (16 * P)) * P + (t % P);
         wf[t] = *reinterpret_cast<const uint2*>(wl + u * 512 + (((g >> 1) * 16 + c) << 4) + ((g & 1) << 3));
-        ws[t] = scale(w_scale(t, c), g >> 1);
+        ws[t] = scale(w_scale(t, c), g >> 1, w_shift >> (2 * t) & 3);
       }
 #pragma unroll
       for (int t = 0; t < S::TW; t++) {
@@ -347,7 +376,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     }
   };
   // the ring's buffers are taken in turn, by loops that are unrolled so that they are constants
-  constexpr bool PAIRS = S::MX && S::SCALES == kWindows;  // K is whole windows of two stages
+  constexpr bool PAIRS = S::MX && !S::SHIFT;  // windows of two stages
   constexpr int UNROLL = PAIRS && S::D % 2 ? 2 * S::D : S::D;
   for (int st0 = 0; st0 < steps; st0 += UNROLL) {
 #pragma unroll
@@ -362,54 +391,21 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   wait_loads<0>();  // nothing writes LDS after the workgroup
 
   if constexpr (!SWIGLU) {
-    if (vec && n0 + S::BN <= N) {
-      wait_loads_barrier<0>();  // the other waves have read their last stage
-      if (a.y_type == MXFP4_F32)
-        store_tile<S, GROUPED, 4>(a, smem + wave * store_bytes<S>(), acc, wx, m0, slot0, rows_m, n0 + ww * S::TW * 16);
-      else
-        store_tile<S, GROUPED, 2>(a, smem + wave * store_bytes<S>(), acc, wx, m0, slot0, rows_m, n0 + ww * S::TW * 16);
-      return;
-    }
+    wait_loads_barrier<0>();  // the other waves have read their last stage
+    const int64_t n = n0 + ww * S::TW * 16;
+    uint8_t* const out = smem + wave * store_bytes<S>();
+    if (n >= N) return;
+    if (a.y_type == MXFP4_F32)
+      store_tile<S, GROUPED, 4>(a, out, acc, wx, m0, slot0, rows_m, n, N - n, vec);
+    else
+      store_tile<S, GROUPED, 2>(a, out, acc, wx, m0, slot0, rows_m, n, N - n, vec);
+    return;
   }
 #pragma unroll
   for (int x = 0; x < S::TX; x++) {
     const int r = (wx * S::TX + x) * 16 + c;
     const bool ok = r < rows_m;
     const int64_t row = GROUPED ? (ok ? a.sorted[slot0 + r] : 0) : m0 + r;
-    if (!SWIGLU) {
-#pragma unroll
-      for (int grp = 0; grp < GROUPS; grp++) {
-        const int64_t n = n0 + w_local(grp * P, 4 * g);
-        if (!ok) continue;
-        if (vec && n + 4 * P <= N) {
-          if (a.y_type == MXFP4_F32) {
-            f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + row * a.ldy + n);
-#pragma unroll
-            for (int s = 0; s < P; s++) d[s] = acc[grp * P + s][x];
-          } else {
-            u32x4* d = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.y) + row * a.ldy + n);
-#pragma unroll
-            for (int s = 0; s < P; s += 2) {
-              const f32x4 u = acc[grp * P + s][x], v = acc[grp * P + s + 1][x];
-              d[s / 2] = u32x4{bf16_pair(u[0], u[1]), bf16_pair(u[2], u[3]), bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-            }
-          }
-          continue;
-        }
-#pragma unroll
-        for (int s = 0; s < P; s++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            if (n + 4 * s + i >= N) continue;
-            const float v = acc[grp * P + s][x][i];
-            if (a.y_type == MXFP4_F32)
-              static_cast<float*>(a.y)[row * a.ldy + n + 4 * s + i] = v;
-            else
-              static_cast<uint16_t*>(a.y)[row * a.ldy + n + 4 * s + i] = (uint16_t)bf16_pair(v, 0.f);
-          }
-      }
-      continue;
-    }
     // SwiGLU: tile t and tile P + t are gate and up of the same columns
     const int64_t n = n0 + w_local(0, 4 * g);
     uint32_t h[2 * P];  // BF16 pairs of 4P consecutive columns
@@ -480,13 +476,10 @@ template <int ACT, int BM, int BN, int WX, int WW, int D>
 hipError_t launch_scales(const MxArgs& a, hipStream_t stream) {
   constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
   const uintptr_t at = (uintptr_t)a.w_scales | (MX ? (uintptr_t)a.x_scales : 0);
-  if (a.K % 512 == 0 && at % 16 == 0)
-    return launch_shape<Shape<ACT, BM, BN, WX, WW, D, kWindows>>(a, stream);
-  if constexpr (MX) {
-    if (a.K % 128 == 0 && at % 4 == 0) return launch_shape<Shape<ACT, BM, BN, WX, WW, D, kDwords>>(a, stream);
-  }
-  // (two stages of the largest MXFP4 tile do not fit with byte scales)
-  return launch_shape<Shape<ACT, (MX && BM * BN == 256 * 256 ? 128 : BM), BN, WX, WW, D, kBytes>>(a, stream);
+  return a.K % (MX ? 256 : 128) == 0 && at % 4 == 0
+             ? launch_shape<Shape<ACT, BM, BN, WX, WW, D, false>>(a, stream)
+             // (the largest MXFP4 tile has no registers left for the shifts)
+             : launch_shape<Shape<ACT, (MX && BM * BN == 256 * 256 ? 128 : BM), BN, WX, WW, D, true>>(a, stream);
 }
 
 template <int ACT>
