@@ -40,6 +40,15 @@ struct Cfg {
   static_assert(NT <= 4 && TM <= 4 && LDS <= 160 * 1024, "");
 };
 
+// slot of piece q of a 64-byte row is q ^ code_swizzle(row), of a 256-byte one piece_slot(q) ^
+// row % 16: a 16-byte LDS read takes rows 0..3 and 12..15 of lanes with one g and rows 4..11 of
+// those with the next one together
+__device__ __forceinline__ int code_swizzle(int row) {
+  const int a = (row >> 2) & 3;
+  return ((a & 1) << 1) ^ ((a >> 1) * 3);
+}
+__device__ __forceinline__ int piece_slot(int q) { return (q & 3) << 2 | q >> 2; }  // its own inverse
+
 struct Operands {
   u32x4 w, ws, x, xs;  // descriptors
 };
@@ -53,7 +62,7 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
   constexpr int XI = C::XMAX, LOADS = C::NT + XI + C::SW + C::SX;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   // this lane's block of a load of codes, and its 16-byte piece of a load of BF16 rows
-  const int wq = (lane & 3) ^ ((lane >> 4) & 3);
+  const int wq = (lane & 3) ^ code_swizzle(lane >> 2);
   const auto issue = [&](int s, int u) {
     const uint32_t base = ring + u * C::STEP;
     const bool in = s < s1;
@@ -67,7 +76,7 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
       if (C::MX) {
         off = w_at == kOutOfRange ? kOutOfRange : xo[i] + w_at;
       } else {
-        const int q = (lane & 15) ^ ((4 * i + (lane >> 4)) & 15);  // of the row's 16 pieces
+        const int q = piece_slot((lane & 15) ^ ((4 * i + (lane >> 4)) & 15));  // of the row's 16
         off = in && 4 * s + (q >> 2) < nb ? xo[i] + 256 * s : kOutOfRange;
       }
       lds_load<16>(d.x, off, base + C::X0 + 1024 * i);
@@ -103,12 +112,12 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
       uint32_t xs[C::TM];
 #pragma unroll
       for (int x = 0; x < C::TM; x++) {
-        xf[x] = *reinterpret_cast<const u32x4*>(b + C::X0 + 1024 * x + 64 * c + ((g ^ (c >> 2)) << 4));
+        xf[x] = *reinterpret_cast<const u32x4*>(b + C::X0 + 1024 * x + 64 * c + ((g ^ code_swizzle(c)) << 4));
         xs[x] = scale(C::SW, 16 * x + c);
       }
 #pragma unroll
       for (int t = 0; t < C::NT; t++) {
-        const u32x4 wf = *reinterpret_cast<const u32x4*>(b + C::W0 + 1024 * t + 64 * c + ((g ^ (c >> 2)) << 4));
+        const u32x4 wf = *reinterpret_cast<const u32x4*>(b + C::W0 + 1024 * t + 64 * c + ((g ^ code_swizzle(c)) << 4));
         const uint32_t ws = scale(0, 16 * t + c);
 #pragma unroll
         for (int x = 0; x < C::TM; x++) acc[t][x] = mfma_mx(wf, xf[x], acc[t][x], ws, xs[x]);
@@ -121,11 +130,11 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
         const int r = (16 * x + c) % (4 * XI);
 #pragma unroll
         for (int j = 0; j < 4; j++)
-          xf[x][j] = *reinterpret_cast<const u32x4*>(b + C::X0 + 256 * r + (((4 * g + j) ^ (r & 15)) << 4));
+          xf[x][j] = *reinterpret_cast<const u32x4*>(b + C::X0 + 256 * r + (((g + 4 * j) ^ (r & 15)) << 4));
       }
 #pragma unroll
       for (int t = 0; t < C::NT; t++) {
-        const u32x4 wf = *reinterpret_cast<const u32x4*>(b + C::W0 + 1024 * t + 64 * c + ((g ^ (c >> 2)) << 4));
+        const u32x4 wf = *reinterpret_cast<const u32x4*>(b + C::W0 + 1024 * t + 64 * c + ((g ^ code_swizzle(c)) << 4));
         const float ws = e8m0_operand(scale(0, 16 * t + c));
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -259,7 +268,7 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
     const int n = n0 + 16 * (t % NO) + i;
     return n < cols ? n - r0 + (t >= NO ? half : 0) : -1;
   };
-  const int wq = (lane & 3) ^ ((lane >> 4) & 3);
+  const int wq = (lane & 3) ^ code_swizzle(lane >> 2);
   uint32_t wo[C::NT], wso[C::SW];
 #pragma unroll
   for (int t = 0; t < C::NT; t++) {
@@ -306,7 +315,7 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
 #pragma unroll
     for (int i = 0; i < C::XMAX; i++) {
       const int row = x_row(C::MX ? 16 * i + (lane >> 2) : 4 * i + (lane >> 4));
-      const int q = C::MX ? wq : (lane & 15) ^ ((4 * i + (lane >> 4)) & 15);
+      const int q = C::MX ? wq : piece_slot((lane & 15) ^ ((4 * i + (lane >> 4)) & 15));
       xo[i] = row >= 0 ? (uint32_t)row * xpitch + 16 * q : kOutOfRange;
       if (C::MX && !C::DW) xso[i] = row >= 0 ? (uint32_t)row * nb + (lane & 3) : kOutOfRange;
     }
@@ -343,13 +352,26 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
       const f32x4 v = total(t, x);
       if (!SWIGLU) {
         if (!ok) continue;
+        const int64_t at = row * a.ldy + n;
+        if (a.y_type == MXFP4_F32) {
+          float* y = static_cast<float*>(a.y) + at;
+          if (n + 4 <= N && ((uintptr_t)y & 15) == 0) {
+            *reinterpret_cast<f32x4*>(y) = v;
+          } else {
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-          if (n + q >= N) continue;
-          if (a.y_type == MXFP4_F32)
-            static_cast<float*>(a.y)[row * a.ldy + n + q] = v[q];
-          else
-            static_cast<uint16_t*>(a.y)[row * a.ldy + n + q] = (uint16_t)bf16_pair(v[q], 0.f);
+            for (int q = 0; q < 4; q++)
+              if (n + q < N) y[q] = v[q];
+          }
+        } else {
+          uint16_t* y = static_cast<uint16_t*>(a.y) + at;
+          const uint2 b = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+          if (n + 4 <= N && ((uintptr_t)y & 7) == 0) {
+            *reinterpret_cast<uint2*>(y) = b;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+              if (n + q < N) y[q] = (uint16_t)((q < 2 ? b.x : b.y) >> (16 * (q & 1)));
+          }
         }
         continue;
       }
