@@ -65,13 +65,22 @@ int64_t x_pitch(int32_t act_kind, int64_t ldx, int64_t K) {
   return act_kind == MXFP4_ACT_MXFP4 ? K / 2 : ldx * 2;
 }
 
+// Whether a dense product streams the weight (for runs of 64 rows, K split between the waves of
+// a workgroup) or takes LDS tiles. Up to 32 rows the weight is read once. For more, what
+// counts is how many runs of 64 rows x 32 columns there are for 256 CUs: with K = 4096, BF16
+// activations, 256 of them (128 x 4096) take 13.5 us against 29.0 in tiles, 512 (256 x 4096)
+// 24.7 against 29.4, 768 (128 x 12288) 36.2 against 29.8; with MXFP4 ones 256 take 10.5
+// against 13.5, 384 (64 x 12288) 15.9 against 13.6.
+bool streams(int32_t act_kind, int64_t M, int64_t N) {
+  return M <= 32 || (M + 63) / 64 * ((N + 31) / 32) <= (act_kind == MXFP4_ACT_BF16 ? 550 : 300);
+}
+
 // How the grouped call goes about R = T * top_k routes. It depends on nothing else, so that
 // both calls of a layer agree on the workspace's grouping.
 //  - scan: few routes; each workgroup looks for its expert in topk_ids and nothing is grouped.
 //  - slots: less than kTiledRoutes routes per active expert on average; the weight is
 //    streamed for up to 16 routes, experts with more have the rest in the list of tiles.
 //  - tiles of 64 or 128 routes for more.
-constexpr int64_t kStreamRows = 64;   // dense: rows that the streaming kernel takes
 constexpr int64_t kTiledRoutes = 16;
 constexpr int64_t kTile128Routes = 96;
 
@@ -178,7 +187,7 @@ nvfp4_status mxfp4_linear(int32_t act_kind, const void* x, const uint8_t* x_scal
   a.w_codes = w_codes; a.w_scales = w_scales;
   a.M = a.x_rows = M; a.N = N; a.K = K;
   a.y = y; a.ldy = ldy; a.y_type = y_type;
-  return launch_status(M <= kStreamRows ? launch_mx_stream(a, act_kind, M, s) : launch_mx_tiled(a, act_kind, s));
+  return launch_status(streams(act_kind, M, N) ? launch_mx_stream(a, act_kind, M, s) : launch_mx_tiled(a, act_kind, s));
 }
 
 nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t* x_scales,

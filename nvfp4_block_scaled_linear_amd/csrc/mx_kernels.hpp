@@ -54,8 +54,8 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 
 // LDS tiles (mx_tiled.hip): dense, or the grouping's list of tiles of tile_rows routes
 hipError_t launch_mx_tiled(const MxArgs& a, int act_kind, hipStream_t stream);
-// the weight streamed (mx_stream.hip) for about `rows` activation rows per weight (dense: M
-// of them, at most 64), the grouped form by ids or by slots
+// the weight streamed (mx_stream.hip) for about `rows` activation rows per weight (dense: M of
+// them), the grouped form by ids or by slots
 hipError_t launch_mx_stream(const MxArgs& a, int act_kind, int64_t rows, hipStream_t stream);
 // most routes in all that the form by ids takes, and the routes of a slot or a list tile of
 // the other

@@ -471,7 +471,6 @@ hipError_t launch_shape(const MxArgs& a, hipStream_t stream) {
 
 constexpr int64_t kFewTiles = 200;
 
-//LAUNCH
 template <int ACT, int BM, int BN, int WX, int WW, int D>
 hipError_t launch_scales(const MxArgs& a, hipStream_t stream) {
   constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
@@ -497,7 +496,6 @@ hipError_t launch_act(const MxArgs& a, hipStream_t stream) {
   if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_scales<ACT, 128, 128, 2, 2, MX ? 3 : 4>(a, stream);
   return launch_scales<ACT, 64, 128, 2, 2, MX ? 3 : 4>(a, stream);
 }
-//END
 
 }  // namespace
 

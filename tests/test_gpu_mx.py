@@ -200,6 +200,69 @@ def test_linear(dev, M, N, K, kind):
     assert torch.equal(nv.mxfp4_linear(xd, cd, sd, x_scales=xs), y)  # the same on every run
 
 
+# enough rows and columns for LDS tiles of 64 x 128, 128 x 128, 128 x 256 and 256 x 256, ragged
+# in both, each with K of whole stages, of a part of one, and with scale rows off the dword
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("K", [32, 160, 256, 416, 768, 1536])
+@pytest.mark.parametrize("M,N", [(330, 4001), (1000, 3300), (1500, 4404), (2500, 5400)])
+def test_linear_tiles(dev, M, N, K, kind):
+    say("linear tiles", kind, M, N, K)
+    rng = rng_of(15, M, N, K)
+    x, (c, s) = acts(rng, M, K), weight(rng, N, K)
+    (xd, xs), xv = act_operand(x, kind, dev)
+    keep = np.unique(np.concatenate([np.arange(0, M, 37), [M - 1, M - 2]]))  # rows for the reference
+    want, mag = ref.linear(xv[keep], ref.dequantize(c, s))
+    cd, sd = up(c, dev), up(s, dev)
+    y = nv.mxfp4_linear(xd, cd, sd, x_scales=xs)
+    assert_near(y[torch.from_numpy(keep).to(dev)], want, ref.tolerance(want, mag, K), (kind, M, N, K))
+    # every row against the same rows in calls of 32, which stream the weight: both are within
+    # the tolerance of the true value; the magnitudes from the codes without their signs
+    parts = torch.cat([nv.mxfp4_linear(xd[i:i + 32], cd, sd, x_scales=None if xs is None else xs[i:i + 32]) for i in range(0, M, 32)])
+    mags = num(nv.mxfp4_linear(xd.abs() if xs is None else xd & 0x77, cd & 0x77, sd, x_scales=xs)) * 1.01
+    assert_near(y, num(parts), 2 * ref.tolerance(num(parts), mags, K), "rows")
+    yb = nv.mxfp4_linear(xd, cd, sd, x_scales=xs, out_dtype=torch.bfloat16)
+    assert torch.equal(yb, y.bfloat16())
+    buf = torch.full((s.size + 3,), 255, dtype=torch.uint8, device=dev)
+    off = buf[3:].view(N, K // 32)
+    off.copy_(sd)
+    wide = torch.full((M, N + 3), 5.0, device=dev)
+    nv.mxfp4_linear(xd, cd, off, x_scales=xs, out=wide[:, 1:1 + N])
+    assert_near(wide[:, 1:1 + N], num(y), 2 * ref.tolerance(num(y), mags, K), "offset scales and columns")
+    assert (wide[:, 0] == 5).all() and (wide[:, N + 1:] == 5).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T,E,k,N,K", [(4200, 8, 2, 1088, 416), (1800, 3, 2, 640, 768), (2100, 40, 2, 576, 288)])
+def test_grouped_tiles(dev, T, E, k, N, K, kind):
+    """Prompt-sized groups: rows against float64, the other forms against the rows."""
+    say("grouped tiles", kind, T, E, k, N, K)
+    rng = rng_of(16, T, E)
+    ids, tw = routes(rng, T, E, k)
+    ids[5] = -1
+    x, (c, s) = acts(rng, T, K), weight(rng, E, N, K)
+    (xd, xs), xv = act_operand(x, kind, dev)
+    args = (xd, up(c, dev), up(s, dev), up(ids, dev))
+    rows = nv.mxfp4_grouped_linear(*args, x_scales=xs)
+    flat, tok = ids.reshape(-1), np.arange(T * k) // k
+    for e in (0, E // 2, E - 1):
+        mine = np.flatnonzero(flat == e)[::11]
+        y, mag = ref.linear(xv[tok[mine]], ref.dequantize(c[e], s[e]))
+        assert_near(rows[torch.from_numpy(mine).to(dev)], y, ref.tolerance(y, mag, K), ("expert", e))
+    assert not rows[5 * k:6 * k].any()
+    assert torch.equal(nv.mxfp4_grouped_linear(*args, x_scales=xs, out_dtype=torch.bfloat16), rows.bfloat16())
+    a = nv.mxfp4_grouped_linear(*args, x_scales=xs, out_mode=nv.OUT_SWIGLU_BF16)
+    h = num(rows)
+    want, t = ref.swiglu(h, 0 * h, N // 2)
+    assert_near(a, want, t + 2.0 ** -8 * (np.abs(want) + t) + 1e-37, "swiglu")
+    if N % 64 == 0:
+        qc, qs = nv.mxfp4_grouped_linear(*args, x_scales=xs, out_mode=nv.OUT_SWIGLU_MXFP4)
+        rc, rs = nv.mxfp4_quantize(a)
+        assert torch.equal(qs, rs) and torch.equal(qc, rc)
+    out = num(nv.mxfp4_grouped_linear(*args, x_scales=xs, topk_w=up(tw, dev), out_mode=nv.OUT_COMBINE))
+    terms = h.reshape(T, k, N) * tw[..., None].astype(np.float64)
+    assert np.all(np.abs(out - terms.sum(1)) <= (k + 1) * 2.0 ** -24 * np.abs(terms).sum(1) + 1e-37)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
 @pytest.mark.parametrize("M", [1, 5, 40, 300])
 def test_linear_pitched_views_and_what_lies_around(dev, M, kind):
@@ -468,7 +531,7 @@ def layer_calls(dev, T, seed):
     return run, [xc, xs, back, y, y16, a, a_s, out]
 
 
-@pytest.mark.parametrize("T", [1, 12, 70, 600])
+@pytest.mark.parametrize("T", [1, 12, 70, 600, 2500])
 def test_graph_replays(dev, T):
     run, outs = layer_calls(dev, T, 0)
     other, _ = layer_calls(dev, T + 3, 1)
