@@ -124,7 +124,7 @@ def _acts(x, x_scales, half, index):
     if x.get_device() != index:
         raise ValueError(f"x is on {x.device}, the weight on cuda:{index}")
     if x_scales is not None:
-        M = x.shape[0]
+        M = x.shape[0] if x.dim() else 0
         return _ACT_MXFP4, M, _dense(x, "x", _U8, (M, half), index), _dense(x_scales, "x_scales", _U8, (M, half >> 4), index), 2 * half
     M, K, ld = _rows(x, "x", _X_TYPES)
     if K != 2 * half:

@@ -255,6 +255,7 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
   a.top_k = top_k; a.num_experts = num_experts;
   a.y = y; a.y_scales = y_scales; a.ldy = N; a.y_type = y_type;
   a.swiglu = swiglu ? out_mode : 0;
+  a.zero_dropped = out_mode != MXFP4_OUT_COMBINE;
   if (out_mode == MXFP4_OUT_COMBINE) {
     a.y = rows;
     a.y_type = MXFP4_F32;
@@ -278,13 +279,9 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
     ws.tile_rows = plan.tile_rows;
     ws.main_rows = plan.main_rows;
     if (!reuse) {
-      // the grouping clears the rows of dropped routes (MXFP4: their codes)
-      const bool keep = out_mode == MXFP4_OUT_COMBINE;
-      const int64_t row_bytes = out_mode == MXFP4_OUT_ROUTES ? N * type_bytes(y_type)
-                                : out_mode == MXFP4_OUT_SWIGLU_BF16 ? N : N / 4;
       e = R <= kMxGroupRoutes
-              ? launch_mx_group(topk_ids, R, top_k, num_experts, ws, faults, keep ? nullptr : y, row_bytes, s)
-              : launch_route_sort(topk_ids, T, top_k, num_experts, ws, faults, keep ? nullptr : y, row_bytes, s);
+              ? launch_mx_group(topk_ids, R, top_k, num_experts, ws, faults, s)
+              : launch_route_sort(topk_ids, T, top_k, num_experts, ws, faults, nullptr, 0, s);
       if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
     }
     a.tile_rows = plan.tile_rows; a.max_tiles = plan.max_tiles; a.max_slots = ws.max_slots;

@@ -17,8 +17,7 @@ constexpr int kThreads = 1024;
 constexpr int kPer = kMxGroupRoutes / kThreads;  // routes of a thread
 
 __global__ __launch_bounds__(kThreads) void mx_group(const int32_t* ids, int R, int top_k, int E,
-                                                     RouteWorkspace ws, uint32_t* faults,
-                                                     uint16_t* zero_out, int64_t zero_bytes) {
+                                                     RouteWorkspace ws, uint32_t* faults) {
   extern __shared__ int32_t sh[];
   int32_t* id = sh;          // [R]
   int32_t* cnt = sh + R;     // [E] routes, then first place in `sorted`
@@ -41,8 +40,6 @@ __global__ __launch_bounds__(kThreads) void mx_group(const int32_t* ids, int R, 
     }
     ws.route_expert[r] = -1;
     if (faults) atomicOr(faults, (uint32_t)NVFP4_FAULT_BAD_ROUTE);
-    if (zero_out)
-      for (int64_t b = 0; b < zero_bytes >> 1; b++) zero_out[r * (zero_bytes >> 1) + b] = 0;
   }
   __syncthreads();
   int32_t run[3] = {0, 0, 0};  // routes, active experts and tiles of the experts so far
@@ -107,11 +104,9 @@ __global__ __launch_bounds__(kThreads) void mx_group(const int32_t* ids, int R, 
 }  // namespace
 
 hipError_t launch_mx_group(const int32_t* topk_ids, int64_t R, int top_k, int E,
-                           const RouteWorkspace& ws, uint32_t* faults, void* zero_out,
-                           int64_t zero_row_bytes, hipStream_t stream) {
+                           const RouteWorkspace& ws, uint32_t* faults, hipStream_t stream) {
   hipLaunchKernelGGL(mx_group, dim3(1), dim3(kThreads), sizeof(int32_t) * (size_t)(R + 2 * E),
-                     stream, topk_ids, (int)R, top_k, E, ws, faults,
-                     static_cast<uint16_t*>(zero_out), zero_row_bytes);
+                     stream, topk_ids, (int)R, top_k, E, ws, faults);
   return hipGetLastError();
 }
 

@@ -30,6 +30,7 @@ struct MxArgs {
   const int32_t* ids;      // topk_ids, where the kernel finds the routes itself (else NULL)
   int32_t num_experts;
   uint32_t* faults;        // with ids
+  int32_t zero_dropped;    // rows of dropped routes are written (as zeros)
   // otherwise the grouping: slot records of the experts, tiles of routes
   int32_t tile_rows;       // routes of a list tile
   int64_t max_tiles;       // bounds of the lists
@@ -62,11 +63,10 @@ hipError_t launch_mx_stream(const MxArgs& a, int act_kind, int64_t rows, hipStre
 int64_t mx_scan_routes();
 constexpr int kMxSlotRoutes = 16;
 
-// groups up to kMxGroupRoutes routes; what launch_route_sort writes, and it clears dropped rows
+// groups up to kMxGroupRoutes routes; what launch_route_sort writes
 constexpr int kMxGroupRoutes = 4096;
 hipError_t launch_mx_group(const int32_t* topk_ids, int64_t R, int top_k, int E,
-                           const RouteWorkspace& ws, uint32_t* faults, void* zero_out,
-                           int64_t zero_row_bytes, hipStream_t stream);
+                           const RouteWorkspace& ws, uint32_t* faults, hipStream_t stream);
 
 // y[t] = sum over t's kept routes in ascending expert id of topk_w * rows[route], N columns of
 // rows of `pitch` and ldy values

@@ -226,7 +226,7 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
   const int row0 = MODE == kDense ? group * C::XR : 0;
   if (MODE == kDense) count = (int)a.M - row0 < C::XR ? (int)a.M - row0 : C::XR;
   if (MODE == kByExpert) {
-    if (blockIdx.x == 0) drop_routes<SWIGLU>(a);
+    drop_routes<SWIGLU>(a);
     if (!scan_routes(a.ids, (int)a.R, a.top_k, a.num_experts, group, &e, kept)) return;
     count = 0;
 #pragma unroll
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
     if (count == 0) return;
   }
   if (MODE == kBySlot) {
-    if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4) clear_dropped_scales(a);
+    clear_dropped<SWIGLU>(a);
     if (group < a.max_slots) {
       const int32_t v = lane < kSlotInts ? a.slots[(int64_t)kSlotInts * group + lane] : 0;
       e = __builtin_amdgcn_readlane(v, 0);

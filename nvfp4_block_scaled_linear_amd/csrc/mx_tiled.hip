@@ -148,7 +148,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   int64_t mt, nt;
   {
     const int64_t nbm = GROUPED ? *a.n_tiles : (a.M + S::BM - 1) / S::BM;
-    if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4) clear_dropped_scales(a);
+    if (GROUPED) clear_dropped<SWIGLU>(a);
     const int64_t total = nbm * nbn;
     if (blockIdx.x >= total) return;
     const int64_t q = total / 8, r = total % 8, x = blockIdx.x % 8;

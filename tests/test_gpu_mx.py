@@ -450,6 +450,39 @@ def test_grouped_bad_routes(dev, T, E, k, kind):
     assert_near(comb, want, t, "combine")
 
 
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T,E,k", [(24, 40, 5), (300, 40, 3), (400, 7, 4), (2500, 4, 2)])
+@pytest.mark.parametrize("real", [0, 1, 0.4])
+def test_grouped_padded_batch(dev, T, E, k, kind, real):
+    """A batch whose last tokens have no expert: zeros there in every form, whatever lay there,
+    and the other tokens' rows as in a batch of theirs alone."""
+    K, n = 96, int(T * real) if real < 1 else 1
+    rng = rng_of(14, T)
+    ids, tw = routes(rng, T, E, k)
+    ids[n:] = -1
+    x = acts(rng, T, K)
+    (xd, xs), xv = act_operand(x, kind, dev)
+    ids_d, tw_d = up(ids, dev), up(tw, dev)
+    for N, mode, dtype in ((193, nv.OUT_ROUTES, torch.bfloat16), (193, nv.OUT_ROUTES, torch.float32),
+                           (130, nv.OUT_SWIGLU_BF16, torch.bfloat16), (134, nv.OUT_SWIGLU_BF16, torch.bfloat16),
+                           (192, nv.OUT_SWIGLU_MXFP4, torch.uint8), (193, nv.OUT_COMBINE, torch.float32)):
+        c, s = weight(rng, E, N, K)
+        per = 1 if mode == nv.OUT_COMBINE else k
+        cols = {nv.OUT_SWIGLU_BF16: N // 2, nv.OUT_SWIGLU_MXFP4: N // 4}.get(mode, N)
+        out = torch.full((T * per, cols), 77, dtype=dtype, device=dev)
+        osc = torch.full((T * k, N // 64), 77, dtype=torch.uint8, device=dev) if mode == nv.OUT_SWIGLU_MXFP4 else None
+        word = torch.zeros(1, dtype=torch.int32, device=dev)
+        cd, sd = up(c, dev), up(s, dev)
+        nv.mxfp4_grouped_linear(xd, cd, sd, ids_d, topk_w=tw_d, x_scales=xs, out_mode=mode, out=out, out_scales=osc, faults=word)
+        assert int(word) == nv.FAULT_BAD_ROUTE
+        assert not out[n * per:].any() and (osc is None or not osc[n * k:].any())
+        if mode == nv.OUT_ROUTES and dtype == torch.float32 and n:
+            y, mag, _ = route_rows(xv[:n], ref.dequantize(c, s), ids[:n], False)
+            assert_near(out[:n * k], y, ref.tolerance(y, mag, K), "kept rows")
+        elif n:
+            assert out[:n * per].any()
+
+
 def test_grouped_all_on_one_expert_and_one_row_each(dev):
     N, K, E = 96, 128, 40
     rng = rng_of(12)
