@@ -469,16 +469,23 @@ hipError_t launch_shape(const MxArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The largest tile that still makes about a workgroup per CU is taken: larger ones read the
+// operands less often. BF16 activations: decoding a weight (v_cvt_scalef32_pk_bf16_fp4, two
+// values) takes about as long as an MFMA, and each of the WX waves that share weight rows
+// decodes them for itself, so few waves stand side by side along the activations, each with
+// many rows. 2048 x 14336 x 4096 takes 196 us with 2 x 4 waves, 202 with 4 x 2; 512 tokens x
+// top-4 of 32 experts, 2048 x 2048, 42.6 in tiles of 64 x 256 by 1 x 4 waves, 46.7 in 64 x 128
+// by 2 x 2.
 constexpr int64_t kFewTiles = 200;
 
 template <int ACT, int BM, int BN, int WX, int WW, int D>
 hipError_t launch_scales(const MxArgs& a, hipStream_t stream) {
-  constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
+  constexpr bool MX = ACT == MXFP4_ACT_MXFP4, BIG = BM * BN == 256 * 256;
   const uintptr_t at = (uintptr_t)a.w_scales | (MX ? (uintptr_t)a.x_scales : 0);
   return a.K % (MX ? 256 : 128) == 0 && at % 4 == 0
              ? launch_shape<Shape<ACT, BM, BN, WX, WW, D, false>>(a, stream)
-             // (the largest MXFP4 tile has no registers left for the shifts)
-             : launch_shape<Shape<ACT, (MX && BM * BN == 256 * 256 ? 128 : BM), BN, WX, WW, D, true>>(a, stream);
+             // (the largest tiles have no registers left for the shifts)
+             : launch_shape<Shape<ACT, (MX && BIG ? 128 : BM), BN, (!MX && BIG ? 4 : WX), (!MX && BIG ? 2 : WW), D, true>>(a, stream);
 }
 
 template <int ACT>
@@ -491,9 +498,11 @@ hipError_t launch_act(const MxArgs& a, hipStream_t stream) {
     return (a.tiles ? a.max_tiles : (a.M + bm - 1) / bm) * ((cols + bc - 1) / bc);
   };
   const int64_t rows = a.tiles ? a.tile_rows : a.M;
-  if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_scales<ACT, 256, 256, MX ? 2 : 4, MX ? 4 : 2, MX ? 2 : 3>(a, stream);
-  if (rows > 64 && tiles(128, 256) >= kFewTiles) return launch_scales<ACT, 128, 256, MX ? 2 : 4, MX ? 4 : 2, MX ? 2 : 4>(a, stream);
+  if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_scales<ACT, 256, 256, 2, 4, MX ? 2 : 3>(a, stream);
+  if (rows > 64 && tiles(128, 256) >= kFewTiles) return launch_scales<ACT, 128, 256, 2, 4, MX ? 2 : 4>(a, stream);
   if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_scales<ACT, 128, 128, 2, 2, MX ? 3 : 4>(a, stream);
+  if constexpr (!MX)
+    if (tiles(64, 256) >= kFewTiles) return launch_scales<ACT, 64, 256, 1, 4, 3>(a, stream);
   return launch_scales<ACT, 64, 128, 2, 2, MX ? 3 : 4>(a, stream);
 }
 
