@@ -144,15 +144,21 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   const int64_t nbn = (cols + BC - 1) / BC;
 
   // tile of this workgroup: each XCD (blockIdx % 8) takes a run of tiles, which share
-  // operands through its L2
+  // operands through its L2 (the parts of a list tile among them)
   int64_t mt, nt;
+  int part = 0;
   {
+    const int parts = GROUPED ? a.tile_rows / S::BM : 1;
     const int64_t nbm = GROUPED ? *a.n_tiles : (a.M + S::BM - 1) / S::BM;
     if (GROUPED) clear_dropped<SWIGLU>(a);
-    const int64_t total = nbm * nbn;
+    const int64_t total = nbm * nbn * parts;
     if (blockIdx.x >= total) return;
     const int64_t q = total / 8, r = total % 8, x = blockIdx.x % 8;
-    const int64_t lin = x * q + (x < r ? x : r) + blockIdx.x / 8;
+    int64_t lin = x * q + (x < r ? x : r) + blockIdx.x / 8;
+    if (GROUPED) {
+      part = (int)(lin % parts);
+      lin /= parts;
+    }
     const int64_t first = lin / (gm * nbn) * gm, in = lin % (gm * nbn);
     const int64_t rows = nbm - first < gm ? nbm - first : gm;
     mt = first + in % rows;
@@ -165,8 +171,9 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   int32_t slot0 = 0;
   if (GROUPED) {
     const int e = a.tiles[2 * mt];
-    slot0 = a.tiles[2 * mt + 1];
+    slot0 = a.tiles[2 * mt + 1] + part * S::BM;
     const int32_t left = a.offsets[e + 1] - slot0;
+    if (left <= 0) return;
     rows_m = left < S::BM ? left : S::BM;
     wc += (int64_t)e * N * (K >> 1);
     ws += (int64_t)e * N * nb;
@@ -455,7 +462,8 @@ hipError_t launch_shape(const MxArgs& a, hipStream_t stream) {
   const int64_t bc = a.swiglu ? S::BN / 2 : S::BN;
   const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
   const int64_t nbm = a.tiles ? a.max_tiles : (a.M + S::BM - 1) / S::BM;
-  const int64_t groups = nbm * ((cols + bc - 1) / bc);
+  const int64_t parts = a.tiles ? a.tile_rows / S::BM : 1;
+  const int64_t groups = nbm * ((cols + bc - 1) / bc) * parts;
   if (groups * S::T > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
   // an XCD's 32 CUs work on gm x (32 / gm) tiles (grouped: on the columns of a few list tiles)
   const int gm = a.tiles ? 1 : S::MX ? 4 : 2;
@@ -475,7 +483,9 @@ hipError_t launch_shape(const MxArgs& a, hipStream_t stream) {
 // decodes them for itself, so few waves stand side by side along the activations, each with
 // many rows. 2048 x 14336 x 4096 takes 196 us with 2 x 4 waves, 202 with 4 x 2; 512 tokens x
 // top-4 of 32 experts, 2048 x 2048, 42.6 in tiles of 64 x 256 by 1 x 4 waves, 46.7 in 64 x 128
-// by 2 x 2.
+// by 2 x 2. In a grouped product two tiles of 64 rows then stand for one of 128 on the list:
+// 1024 tokens take 66 to 70 us, in tiles of 128 75. MXFP4 activations have no such cost: 512
+// tokens 27.5 in tiles of 128 rows, 32.5 in tiles of 64.
 constexpr int64_t kFewTiles = 200;
 
 template <int ACT, int BM, int BN, int WX, int WW, int D>
@@ -492,17 +502,17 @@ template <int ACT>
 hipError_t launch_act(const MxArgs& a, hipStream_t stream) {
   constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
   const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
-  // workgroups that tiles of bm rows and bn weight rows make
+  const int64_t active = a.R < a.num_experts ? a.R : a.num_experts;
+  // workgroups that tiles of bm rows and bn weight rows make (grouped: about)
   const auto tiles = [&](int64_t bm, int64_t bn) {
     const int64_t bc = a.swiglu ? bn / 2 : bn;
-    return (a.tiles ? a.max_tiles : (a.M + bm - 1) / bm) * ((cols + bc - 1) / bc);
+    return (a.tiles ? a.R / bm + active : (a.M + bm - 1) / bm) * ((cols + bc - 1) / bc);
   };
-  const int64_t rows = a.tiles ? a.tile_rows : a.M;
+  const int64_t rows = !a.tiles ? a.M : MX ? a.tile_rows : 64;
   if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_scales<ACT, 256, 256, 2, 4, MX ? 2 : 3>(a, stream);
   if (rows > 64 && tiles(128, 256) >= kFewTiles) return launch_scales<ACT, 128, 256, 2, 4, MX ? 2 : 4>(a, stream);
   if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_scales<ACT, 128, 128, 2, 2, MX ? 3 : 4>(a, stream);
-  if constexpr (!MX)
-    if (tiles(64, 256) >= kFewTiles) return launch_scales<ACT, 64, 256, 1, 4, 3>(a, stream);
+  if (tiles(64, 256) >= kFewTiles) return launch_scales<ACT, 64, 256, MX ? 2 : 1, 4, 3>(a, stream);
   return launch_scales<ACT, 64, 128, 2, 2, MX ? 3 : 4>(a, stream);
 }
 
