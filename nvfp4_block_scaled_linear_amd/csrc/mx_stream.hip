@@ -17,6 +17,13 @@
 //    block's scale, and MFMA j is over k = 32g + 8j + [0, 8).
 // Loads past the rows, past K and past a wave's run are out of range: every step issues the
 // same number, which is what the counted waits go by.
+//
+// 16 x 12288 x 4096 with BF16 activations takes 8.8 us (27 MB, 3.0 TB/s), 1 x 2048 x 2048 3.2,
+// 4 x 4096 x 4096 with MXFP4 ones 3.9. Of a layer of 128 experts, top-8, for 16 tokens, gate_up
+// (2048 -> 2 x 768) takes 36.6 us and down (768 -> 2048) 19.9: 3.7 and 3.4 TB/s of the routed
+// experts' weights, in thousands of workgroups that live a few microseconds each, much of that
+// the time to their first load. Rings of several column blocks per workgroup and prefetches into
+// L2 were slower.
 #include "mx_device.hpp"
 #include "mx_kernels.hpp"
 #include "mx_routes.hpp"
@@ -446,7 +453,9 @@ hipError_t launch_rows(const MxArgs& a, hipStream_t stream) {
 
 template <int ACT, int XR, int U>
 hipError_t launch_dense(const MxArgs& a, hipStream_t stream) {
-  const int64_t nt = (a.N + 16 * 256 - 1) / (16 * 256);  // so that a CU has about one workgroup
+  // So that a CU has about one workgroup: 16 x 12288 x 4096 takes 8.9 us with 48 weight rows
+  // (256 workgroups), 11.2 with 16 (768, each loading the activations for itself).
+  const int64_t nt = (a.N + 16 * 256 - 1) / (16 * 256);
   if (nt <= 1) return launch_rows<ACT, XR, 1, 4, U>(a, stream);
   if (nt <= 2) return launch_rows<ACT, XR, 2, 4, U>(a, stream);
   return launch_rows<ACT, XR, 3, 4, U>(a, stream);
@@ -455,6 +464,9 @@ hipError_t launch_dense(const MxArgs& a, hipStream_t stream) {
 template <int ACT>
 hipError_t launch_act(const MxArgs& a, int64_t rows, hipStream_t stream) {
   constexpr bool MX = ACT == MXFP4_ACT_MXFP4;
+  // A BF16 form of four rows loads no activations for the 12 others of the MFMA: 16 tokens x top-8
+  // of 128 experts take 62 us a layer with it, 72 in the form of 16 rows, one token 17.3 and 18.1;
+  // an expert with more routes takes several passes.
   if (a.ids || a.slots) {
     if (a.swiglu) return rows <= 2 ? launch_rows<ACT, MX ? 16 : 4, 4, 4, 2>(a, stream) : launch_rows<ACT, 16, 4, 4, 2>(a, stream);
     return rows <= 2 ? launch_rows<ACT, MX ? 16 : 4, 2, 2, 2>(a, stream) : launch_rows<ACT, 16, 2, 2, 2>(a, stream);
