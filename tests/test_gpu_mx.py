@@ -200,6 +200,42 @@ def test_linear(dev, M, N, K, kind):
     assert torch.equal(nv.mxfp4_linear(xd, cd, sd, x_scales=xs), y)  # the same on every run
 
 
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
+def test_linear_offsets_past_32_bits(dev, kind):
+    """A weight, and activations, of more than 2^31 bytes: 509 rows over and over."""
+    K, P = 8192, 509
+    rng = rng_of(15)
+    c, s = weight(rng, P, K)
+    x = acts(rng, P, K)
+    (xd, xs), xv = act_operand(x, kind, dev)
+    want, mag = ref.linear(xv, ref.dequantize(c, s))
+    tol = ref.tolerance(want, mag, K)
+    cd, sd = up(c, dev), up(s, dev)
+    N = 2 ** 19 + 77
+    which = torch.arange(N, device=dev) % P
+    wc, ws = cd[which], sd[which]
+    cols = np.r_[0:300, N // 2:N // 2 + 300, N - 300:N]
+    for M in (1, 3, 33, 130):
+        say("weight past 2^31 bytes", kind, M)
+        y = nv.mxfp4_linear(xd[:M], wc, ws, x_scales=None if xs is None else xs[:M], out_dtype=torch.float32)
+        assert_near(y[:, cols], want[:M, cols % P], tol[:M, cols % P], ("weight", M))
+    del wc, ws, y
+    M = 2 ** 17 + 77 if kind == "bf16" else 2 ** 19 + 77
+    which = torch.arange(M, device=dev) % P
+    big, bs = xd[which], None if xs is None else xs[which]
+    rows = np.r_[0:300, M // 2:M // 2 + 300, M - 300:M]
+    for N in (1, 70):
+        say("activations past 2^31 bytes", kind, N)
+        y = nv.mxfp4_linear(big, cd[:N], sd[:N], x_scales=bs)
+        assert_near(y[rows], want[rows % P][:, :N], tol[rows % P][:, :N], ("activations", N))
+    if kind == "bf16":
+        qc, qs = nv.mxfp4_quantize(big)
+        rc, rs = (up(a, dev) for a in ref.quantize(num(xd)))
+        assert torch.equal(qc[rows], rc[rows % P]) and torch.equal(qs[rows], rs[rows % P])
+        back = nv.mxfp4_dequantize(qc, qs)
+        assert np.array_equal(num(back[rows]), ref.dequantize(rc.cpu().numpy(), rs.cpu().numpy())[rows % P])
+
+
 # enough rows and columns for LDS tiles of 64 x 128, 128 x 128, 128 x 256 and 256 x 256, ragged
 # in both, each with K of whole stages, of a part of one, and with scale rows off the dword
 @pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
