@@ -21,9 +21,20 @@ _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 _TYPES = {_BF16: 0, _F32: 1}
 _X_TYPES = (_BF16,)
 _lib = None
-# handle of a device's current stream, and the current device, without the objects and checks
-# of torch.cuda's forms, which cost as much as the rest of a call's host work
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _public_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _public_device():
+    return torch.cuda.current_device()
+
+
+# handle of a device's current stream, and the current device: where torch has them without the
+# objects and checks of torch.cuda's forms, which cost as much as the rest of a call's host work
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", _public_device)
 
 
 def _load():
