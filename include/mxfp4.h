@@ -90,6 +90,8 @@ nvfp4_status mxfp4_linear(int32_t act_kind, const void* x, const uint8_t* x_scal
  * topk_ids [T][top_k] int32. Routes, rows_mode, the workspace (NULL: its size is returned in
  * *workspace_bytes), NVFP4_OUT_REUSE_GROUPING, bad routes (NVFP4_FAULT_BAD_ROUTE, dropped)
  * and flags are as in nvfp4_grouped_linear; act_kind, x, x_scales and ldx as in mxfp4_linear.
+ * A reused workspace that does not hold this call's grouping gives unspecified results, but no
+ * access outside the call's buffers, whatever it holds.
  * out_mode MXFP4_OUT_ROUTES: y is [T*top_k][N] of y_type, row r = x_row(r) w_e^T.
  *          MXFP4_OUT_SWIGLU_BF16: N even; y is BF16 [T*top_k][N/2], row r =
  *            bf16_rne(silu(g) * u) with g = h[0:N/2], u = h[N/2:N] of the route's fp32 row

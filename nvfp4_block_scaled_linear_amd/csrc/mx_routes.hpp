@@ -14,6 +14,31 @@ __device__ __forceinline__ bool keeps_route(const int32_t* ids, int64_t r, int t
   return ok;
 }
 
+// A call that reuses a grouping is given a workspace, and one that holds no grouping, or that of
+// other sizes, must not make it leave its buffers: what is read there is an expert, a place or a
+// route only as far as the call has them. (Rows of x need no such care: their loads have a range.)
+__device__ __forceinline__ int32_t in_experts(const MxArgs& a, int32_t e) {
+  const uint32_t last = (uint32_t)a.num_experts - 1;
+  return (int32_t)((uint32_t)e < last ? (uint32_t)e : last);
+}
+
+// how many of the places [first, end) of `sorted`, `most` at most, there are
+__device__ __forceinline__ int run_length(const MxArgs& a, int32_t first, int32_t end, int most) {
+  const int32_t R = (int32_t)a.R;
+  end = end < R ? end : R;
+  if (first < 0 || first >= end) return 0;
+  return end - first < most ? end - first : most;
+}
+
+__device__ __forceinline__ int32_t in_routes(const MxArgs& a, int32_t route) {
+  const uint32_t last = (uint32_t)a.R - 1;
+  return (int32_t)((uint32_t)route < last ? (uint32_t)route : last);
+}
+
+__device__ __forceinline__ int32_t route_at(const MxArgs& a, int32_t place) {
+  return in_routes(a, a.sorted[place]);
+}
+
 // One wave writes zeros over the output row of a dropped route.
 template <int SWIGLU>
 __device__ __forceinline__ void clear_route(const MxArgs& a, int64_t r) {

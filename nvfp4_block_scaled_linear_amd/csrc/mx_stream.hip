@@ -246,20 +246,19 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
       const int32_t v = lane < kSlotInts ? a.slots[(int64_t)kSlotInts * group + lane] : 0;
       e = __builtin_amdgcn_readlane(v, 0);
       if (e < 0) return;
+      e = in_experts(a, e);
       first = __builtin_amdgcn_readlane(v, 1);
-      count = __builtin_amdgcn_readlane(v, 2) - first;
-      count = count < kMxSlotRoutes ? count : kMxSlotRoutes;
+      count = run_length(a, first, __builtin_amdgcn_readlane(v, 2), kMxSlotRoutes);
       const int n = __builtin_amdgcn_readlane(v, 3);
-      my_route = __shfl(v, 4 + c, 64);
-      if (n < count && c >= n && c < count) my_route = a.sorted[first + c];
+      my_route = in_routes(a, __shfl(v, 4 + c, 64));
+      if (n < count && c >= n && c < count) my_route = route_at(a, first + c);
     } else {
       const int tile = group - a.max_slots;
       if (tile >= *a.n_tiles) return;
-      e = a.tiles[2 * tile];
+      e = in_experts(a, a.tiles[2 * tile]);
       first = a.tiles[2 * tile + 1];
-      count = a.offsets[e + 1] - first;
-      count = count < kMxSlotRoutes ? count : kMxSlotRoutes;
-      my_route = c < count ? a.sorted[first + c] : 0;
+      count = run_length(a, first, a.offsets[e + 1], kMxSlotRoutes);
+      my_route = c < count ? route_at(a, first + c) : 0;
     }
   }
   if (GROUPED) {

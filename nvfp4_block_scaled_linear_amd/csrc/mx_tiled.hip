@@ -94,7 +94,7 @@ __device__ __forceinline__ void store_tile(const MxArgs& a, uint8_t* lds, f32x4 
   for (int x = 0; x < S::TX; x++) {
     const int r0 = (wx * S::TX + x) * 16;
     if (r0 >= rows_m) break;
-    const int route = GROUPED && r0 + c < rows_m ? a.sorted[slot0 + r0 + c] : 0;
+    const int route = GROUPED && r0 + c < rows_m ? route_at(a, slot0 + r0 + c) : 0;
 #pragma unroll
     for (int w = 0; w < S::TW; w += ES == 4 ? 1 : 2) {  // one 16-byte piece
       // tiles w .. of group w / 4 hold columns 64 * (w / 4) + 16 * g + 4 * (w % 4) and on
@@ -148,26 +148,30 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   const int64_t N = a.N, K = a.K, half = N >> 1, nb = K >> 5;
   const int64_t cols = SWIGLU ? half : N;
   constexpr int BC = SWIGLU ? S::BN / 2 : S::BN;  // output columns of a tile
-  const int64_t nbn = (cols + BC - 1) / BC;
+  const uint32_t nbn = (uint32_t)((cols + BC - 1) / BC);
 
   // tile of this workgroup: each XCD (blockIdx % 8) takes a run of tiles, which share
-  // operands through its L2 (the parts of a list tile among them)
+  // operands through its L2 (the parts of a list tile among them). There are at most 2^24
+  // tiles; a division in 64 bits takes a hundred instructions.
   int64_t mt, nt;
   int part = 0;
   {
-    const int parts = GROUPED ? a.tile_rows / S::BM : 1;
-    const int64_t nbm = GROUPED ? *a.n_tiles : (a.M + S::BM - 1) / S::BM;
-    if (GROUPED) clear_dropped<SWIGLU>(a);
-    const int64_t total = nbm * nbn * parts;
+    const uint32_t parts = GROUPED ? a.tile_rows / S::BM : 1;
+    uint32_t nbm = GROUPED ? *a.n_tiles : (uint32_t)((a.M + S::BM - 1) / S::BM);
+    if (GROUPED) {
+      nbm = nbm < (uint32_t)a.max_tiles ? nbm : (uint32_t)a.max_tiles;
+      clear_dropped<SWIGLU>(a);
+    }
+    const uint32_t total = nbm * nbn * parts;
     if (blockIdx.x >= total) return;
-    const int64_t q = total / 8, r = total % 8, x = blockIdx.x % 8;
-    int64_t lin = x * q + (x < r ? x : r) + blockIdx.x / 8;
+    const uint32_t q = total / 8, r = total % 8, x = blockIdx.x % 8;
+    uint32_t lin = x * q + (x < r ? x : r) + blockIdx.x / 8;
     if (GROUPED) {
       part = (int)(lin % parts);
       lin /= parts;
     }
-    const int64_t first = lin / (gm * nbn) * gm, in = lin % (gm * nbn);
-    const int64_t rows = nbm - first < gm ? nbm - first : gm;
+    const uint32_t first = lin / (gm * nbn) * gm, in = lin % (gm * nbn);
+    const uint32_t rows = nbm - first < (uint32_t)gm ? nbm - first : gm;
     mt = first + in % rows;
     nt = in / rows;
   }
@@ -177,11 +181,10 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   int64_t m0 = 0, rows_m;
   int32_t slot0 = 0;
   if (GROUPED) {
-    const int e = a.tiles[2 * mt];
-    slot0 = a.tiles[2 * mt + 1] + part * S::BM;
-    const int32_t left = a.offsets[e + 1] - slot0;
-    if (left <= 0) return;
-    rows_m = left < S::BM ? left : S::BM;
+    const int e = in_experts(a, a.tiles[2 * mt]);
+    slot0 = in_routes(a, a.tiles[2 * mt + 1]) + part * S::BM;
+    rows_m = run_length(a, slot0, a.offsets[e + 1], S::BM);
+    if (rows_m == 0) return;
     wc += (int64_t)e * N * (K >> 1);
     ws += (int64_t)e * N * nb;
   } else {
@@ -419,7 +422,7 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   for (int x = 0; x < S::TX; x++) {
     const int r = (wx * S::TX + x) * 16 + c;
     const bool ok = r < rows_m;
-    const int64_t row = GROUPED ? (ok ? a.sorted[slot0 + r] : 0) : m0 + r;
+    const int64_t row = GROUPED ? (ok ? route_at(a, slot0 + r) : 0) : m0 + r;
     // SwiGLU: tile t and tile P + t are gate and up of the same columns
     const int64_t n = n0 + w_local(0, 4 * g);
     uint32_t h[2 * P];  // BF16 pairs of 4P consecutive columns
