@@ -16,7 +16,8 @@ __device__ __forceinline__ bool keeps_route(const int32_t* ids, int64_t r, int t
 
 // A call that reuses a grouping is given a workspace, and one that holds no grouping, or that of
 // other sizes, must not make it leave its buffers: what is read there is an expert, a place or a
-// route only as far as the call has them. (Rows of x need no such care: their loads have a range.)
+// route only as far as the call has them. Rows of x need no such care, their loads have a range: a
+// route is looked at where its row is stored, not on the way to the first loads.
 __device__ __forceinline__ int32_t in_experts(const MxArgs& a, int32_t e) {
   const uint32_t last = (uint32_t)a.num_experts - 1;
   return (int32_t)((uint32_t)e < last ? (uint32_t)e : last);

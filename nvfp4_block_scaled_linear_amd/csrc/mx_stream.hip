@@ -308,15 +308,15 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
       first = __builtin_amdgcn_readlane(v, 1);
       count = run_length(a, first, __builtin_amdgcn_readlane(v, 2), kMxSlotRoutes);
       const int n = __builtin_amdgcn_readlane(v, 3);
-      my_route = in_routes(a, __shfl(v, 4 + c, 64));
-      if (n < count && c >= n && c < count) my_route = route_at(a, first + c);
+      my_route = __shfl(v, 4 + c, 64);
+      if (n < count && c >= n && c < count) my_route = a.sorted[first + c];
     } else {
       const int tile = group - a.max_slots;
       if (tile >= *a.n_tiles) return;
       e = in_experts(a, a.tiles[2 * tile]);
       first = a.tiles[2 * tile + 1];
       count = run_length(a, first, a.offsets[e + 1], kMxSlotRoutes);
-      my_route = c < count ? route_at(a, first + c) : 0;
+      my_route = c < count ? a.sorted[first + c] : 0;
     }
   }
   if (GROUPED) {
@@ -416,7 +416,8 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
     for (int i = wave; i < NO / TS * C::TM; i += C::W) {
       const int t = i % (NO / TS) * TS, x = i / (NO / TS);
       const bool ok = 16 * x + c < rows;
-      const int64_t row = ok ? row0 + y_row(16 * x + c) : 0;
+      int64_t row = 0;
+      if (ok) row = MODE == kBySlot ? in_routes(a, y_row(16 * x + c)) : row0 + y_row(16 * x + c);
       const int n = n0 + 16 * t + 4 * g;
       const f32x4 v = total(t, x);
       if (!SWIGLU) {
