@@ -100,13 +100,13 @@ __device__ __forceinline__ void lds_load(u32x4 rsrc, uint32_t off, uint32_t lds)
   lds = __builtin_amdgcn_readfirstlane(lds);
   if (BYTES == 16)
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory", "m0");
   else if (BYTES == 4)
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_ubyte %0, %1, 0 offen lds"
-                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory", "m0");
 }
 
 // all but this wave's latest N loads are done, and its LDS reads
