@@ -42,11 +42,6 @@ __device__ __forceinline__ u32x4 mx_decode8(uint32_t codes, float scale) {
   return r;
 }
 
-// f32 -> BF16 bits, round to nearest even; NaN stays NaN
-__device__ __forceinline__ uint32_t f32_to_bf16_any(float v) {
-  return v != v ? 0x7FC0u : f32_to_bf16_rne(v);
-}
-
 // two f32 -> BF16 pair, round to nearest even, NaN stays NaN
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

@@ -478,36 +478,42 @@ __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
   }
 }
 
+// A launch names the kernels that it may take and no others: dense forms have no SwiGLU, and among
+// the grouped ones those of four weight tiles have nothing else.
 template <class C, int MODE>
 hipError_t launch_mode(const MxArgs& a, int64_t groups, hipStream_t stream) {
-  const int64_t no = a.swiglu ? C::NT / 2 : C::NT;
-  const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
+  constexpr bool SWIGLU = MODE != kDense && C::NT == 4;
+  constexpr int64_t no = SWIGLU ? C::NT / 2 : C::NT;
+  const int64_t cols = SWIGLU ? a.N >> 1 : a.N;
   const int64_t blocks = (cols + 16 * no - 1) / (16 * no) * groups;
   if (blocks * 64 * C::W > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
-  auto k = mx_stream<C, MODE, 0>;
-  if constexpr (MODE != kDense && C::NT % 4 == 0) {
-    if (a.swiglu == MXFP4_OUT_SWIGLU_BF16) k = mx_stream<C, MODE, MXFP4_OUT_SWIGLU_BF16>;
-    if (a.swiglu == MXFP4_OUT_SWIGLU_MXFP4) k = mx_stream<C, MODE, MXFP4_OUT_SWIGLU_MXFP4>;
-  }
-  hipLaunchKernelGGL(k, dim3((uint32_t)blocks), dim3(64 * C::W), C::LDS, stream, a);
-  return hipGetLastError();
+  const auto launch = [&](auto k) {
+    hipLaunchKernelGGL(k, dim3((uint32_t)blocks), dim3(64 * C::W), C::LDS, stream, a);
+    return hipGetLastError();
+  };
+  if constexpr (SWIGLU)
+    return launch(a.swiglu == MXFP4_OUT_SWIGLU_BF16 ? mx_stream<C, MODE, MXFP4_OUT_SWIGLU_BF16>
+                                                    : mx_stream<C, MODE, MXFP4_OUT_SWIGLU_MXFP4>);
+  else
+    return launch(mx_stream<C, MODE, 0>);
 }
 
-template <class C>
+template <class C, bool GROUPED>
 hipError_t launch_cfg(const MxArgs& a, hipStream_t stream) {
-  if constexpr (C::TM == 1) {
+  if constexpr (GROUPED) {
     static_assert(C::LDS >= 4 * kScanRoutes, "further_run");
-    if (a.ids) return launch_mode<C, kByExpert>(a, scan_groups(a.R, a.top_k, a.num_experts), stream);
-    if (a.slots) return launch_mode<C, kBySlot>(a, a.max_slots + a.max_tiles, stream);
+    return a.ids ? launch_mode<C, kByExpert>(a, scan_groups(a.R, a.top_k, a.num_experts), stream)
+                 : launch_mode<C, kBySlot>(a, a.max_slots + a.max_tiles, stream);
+  } else {
+    return launch_mode<C, kDense>(a, (a.M + C::XR - 1) / C::XR, stream);
   }
-  return launch_mode<C, kDense>(a, (a.M + C::XR - 1) / C::XR, stream);
 }
 
-template <int ACT, int XR, int NT, int W, int U>
+template <int ACT, int XR, int NT, int W, int U, bool GROUPED = false>
 hipError_t launch_rows(const MxArgs& a, hipStream_t stream) {
   const bool dw = a.K % 128 == 0 && ((uintptr_t)a.w_scales | (uintptr_t)a.x_scales) % 4 == 0;
-  return dw ? launch_cfg<Cfg<ACT, XR, NT, W, U, true>>(a, stream)
-            : launch_cfg<Cfg<ACT, XR, NT, W, U, false>>(a, stream);
+  return dw ? launch_cfg<Cfg<ACT, XR, NT, W, U, true>, GROUPED>(a, stream)
+            : launch_cfg<Cfg<ACT, XR, NT, W, U, false>, GROUPED>(a, stream);
 }
 
 template <int ACT, int XR, int U>
@@ -527,8 +533,9 @@ hipError_t launch_act(const MxArgs& a, int64_t rows, hipStream_t stream) {
   // of 128 experts take 62 us a layer with it, 72 in the form of 16 rows, one token 17.3 and 18.1;
   // an expert with more routes takes several passes.
   if (a.ids || a.slots) {
-    if (a.swiglu) return rows <= 2 ? launch_rows<ACT, MX ? 16 : 4, 4, 4, 2>(a, stream) : launch_rows<ACT, 16, 4, 4, 2>(a, stream);
-    return rows <= 2 ? launch_rows<ACT, MX ? 16 : 4, 2, 2, 2>(a, stream) : launch_rows<ACT, 16, 2, 2, 2>(a, stream);
+    constexpr int FEW = MX ? 16 : 4;
+    if (a.swiglu) return rows <= 2 ? launch_rows<ACT, FEW, 4, 4, 2, true>(a, stream) : launch_rows<ACT, 16, 4, 4, 2, true>(a, stream);
+    return rows <= 2 ? launch_rows<ACT, FEW, 2, 2, 2, true>(a, stream) : launch_rows<ACT, 16, 2, 2, 2, true>(a, stream);
   }
   if (rows <= 4) return launch_dense<ACT, MX ? 16 : 4, MX ? 4 : 2>(a, stream);
   if (rows <= 16) return launch_dense<ACT, 16, MX ? 4 : 2>(a, stream);

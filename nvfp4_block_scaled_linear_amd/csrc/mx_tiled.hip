@@ -140,6 +140,7 @@ __global__ __launch_bounds__(S::T) __attribute__((amdgpu_waves_per_eu(S::T == 51
 void mx_tiled(MxArgs a, int gm, int vec) {
   constexpr int P = SWIGLU ? S::TW / 2 : 4;  // tiles of a group of weight rows
   constexpr int GROUPS = S::TW / P;          // of a wave; SwiGLU: gate, up
+  static_assert(SWIGLU == 0 || P == 2, "the 32 columns of a block are 4P in each of four lanes");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -449,10 +450,8 @@ void mx_tiled(MxArgs a, int gm, int vec) {
     uint32_t amax = amax_pairs<2 * P>(h);
     uint32_t o = __shfl_xor(amax, 16, 64);
     amax = amax > o ? amax : o;
-    if (P == 2) {
-      o = __shfl_xor(amax, 32, 64);
-      amax = amax > o ? amax : o;
-    }
+    o = __shfl_xor(amax, 32, 64);
+    amax = amax > o ? amax : o;
     const uint32_t sc = e8m0_of_amax(amax);
     const bool bad = amax >= 0x7F800000u;
     uint32_t code[P / 2];
@@ -467,6 +466,9 @@ void mx_tiled(MxArgs a, int gm, int vec) {
   }
 }
 
+// most rows of a tile of a grouped product
+constexpr int grouped_rows(int act) { return act == MXFP4_ACT_MXFP4 ? 128 : 64; }
+
 template <class S>
 hipError_t launch_shape(const MxArgs& a, hipStream_t stream) {
   const int64_t bc = a.swiglu ? S::BN / 2 : S::BN;
@@ -479,10 +481,13 @@ hipError_t launch_shape(const MxArgs& a, hipStream_t stream) {
   const int gm = a.tiles ? 1 : S::MX ? 4 : 2;
   const int64_t ysz = a.y_type == MXFP4_F32 ? 4 : 2, ld = a.swiglu ? cols : a.ldy;
   const int vec = ((uintptr_t)a.y | (uintptr_t)(ld * ysz)) % 16 == 0;
-  auto k = !a.tiles ? mx_tiled<S, false, 0>
-           : a.swiglu == 0 ? mx_tiled<S, true, 0>
-           : a.swiglu == MXFP4_OUT_SWIGLU_BF16 ? mx_tiled<S, true, MXFP4_OUT_SWIGLU_BF16>
-                                               : mx_tiled<S, true, MXFP4_OUT_SWIGLU_MXFP4>;
+  auto k = mx_tiled<S, false, 0>;
+  if constexpr (S::BM <= grouped_rows(S::ACT)) {
+    if (a.tiles)
+      k = a.swiglu == 0 ? mx_tiled<S, true, 0>
+          : a.swiglu == MXFP4_OUT_SWIGLU_BF16 ? mx_tiled<S, true, MXFP4_OUT_SWIGLU_BF16>
+                                              : mx_tiled<S, true, MXFP4_OUT_SWIGLU_MXFP4>;
+  }
   hipLaunchKernelGGL(k, dim3((uint32_t)groups), dim3(S::T), S::LDS, stream, a, gm, vec);
   return hipGetLastError();
 }
@@ -518,7 +523,7 @@ hipError_t launch_act(const MxArgs& a, hipStream_t stream) {
     const int64_t bc = a.swiglu ? bn / 2 : bn;
     return (a.tiles ? a.R / bm + active : (a.M + bm - 1) / bm) * ((cols + bc - 1) / bc);
   };
-  const int64_t rows = !a.tiles ? a.M : MX ? a.tile_rows : 64;
+  const int64_t rows = !a.tiles ? a.M : a.tile_rows < grouped_rows(ACT) ? a.tile_rows : grouped_rows(ACT);
   if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_scales<ACT, 256, 256, 2, 4, MX ? 2 : 3>(a, stream);
   if (rows > 64 && tiles(128, 256) >= kFewTiles) return launch_scales<ACT, 128, 256, 2, 4, MX ? 2 : 4>(a, stream);
   if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_scales<ACT, 128, 128, 2, 2, MX ? 3 : 4>(a, stream);
