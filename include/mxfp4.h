@@ -11,7 +11,8 @@
  *   codes   [N][K/2]  uint8, byte j of a row holds k = 2j in its low nibble and
  *                      k = 2j+1 in its high nibble; rows contiguous, base 16-byte aligned;
  *   scales  [N][K/32] uint8, any alignment.
- * K % 32 == 0; M, N and T may be any positive size up to 2^22, K likewise. Offsets into
+ * K % 32 == 0; M, N and T * top_k may be any positive size up to 2^22, K likewise; there are at
+ * most 4096 experts, and top_k is at most 64 and at most their number. Offsets into
  * the activations (of a dense call: into 256 rows of them) and into one expert's codes are
  * 32-bit: 2^31 bytes and more are refused (NVFP4_ERR_SHAPE).
  *

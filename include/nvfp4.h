@@ -180,8 +180,9 @@ nvfp4_status nvfp4_quantize_act(int32_t in_type, const void* x, int64_t ldx, int
  *   call of the same layer); the grouping is not recomputed. The grouping occupies the
  *   same leading bytes of the workspace in every output form, so one workspace sized
  *   for the combine serves both calls. Bad routes were reported by the earlier call.
- *   Passing stale topk_ids or a different workspace gives unspecified (but in-bounds)
- *   results. Any other out_mode with this bit is NVFP4_ERR_ARG.
+ *   Passing stale topk_ids gives unspecified (but in-bounds) results; a workspace that
+ *   holds no grouping of this T, top_k and num_experts must not be passed. Any other
+ *   out_mode with this bit is NVFP4_ERR_ARG.
  * Decode-sized batches stream each active expert's weight once for all its routes;
  *   prompt-sized ones (routes averaging >= 32 per active expert) run MFMA tiles of one
  *   expert's routes (the pages' expert-grouped prompt GEMM, each expert read once per

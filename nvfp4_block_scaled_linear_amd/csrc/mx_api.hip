@@ -68,9 +68,13 @@ int64_t x_pitch(int32_t act_kind, int64_t ldx, int64_t K) {
 // Whether a dense product streams the weight (for runs of 64 rows, K split between the waves of
 // a workgroup) or takes LDS tiles. Up to 32 rows the weight is read once. For more, what
 // counts is how many runs of 64 rows x 32 columns there are for 256 CUs: with K = 4096, BF16
-// activations, 256 of them (128 x 4096) take 13.5 us against 29.0 in tiles, 512 (256 x 4096)
-// 24.7 against 29.4, 768 (128 x 12288) 36.2 against 29.8; with MXFP4 ones 256 take 10.5
-// against 13.5, 384 (64 x 12288) 15.9 against 13.6.
+// activations, 256 of them (128 x 4096) take 12.4 us against 29.0 in tiles, 512 (256 x 4096)
+// 23.3 against 30.1, 768 (128 x 12288) 34.2 against 30.2; with MXFP4 ones 256 take 7.1 against
+// 10.7, 384 (64 x 12288) 11.4 against 11.3. Both sides grow with K, and no border in runs serves
+// every K better by more than an eighth: BF16, 512 take 8.7 against 7.8 with K = 512, 15.5 against
+// 17.2 with 2048, 65.5 against 92.6 with 14336, 768 take 12.2 against 7.6 with 512 and 98.6
+// against 93.1 with 14336; MXFP4, 256 take 3.7 against 4.8 with 512 and 24.8 against 28.1 with
+// 14336, 384 take 4.3 against 5.1 and 43.1 against 28.1.
 bool streams(int32_t act_kind, int64_t M, int64_t N) {
   return M <= 32 || (M + 63) / 64 * ((N + 31) / 32) <= (act_kind == MXFP4_ACT_BF16 ? 550 : 300);
 }

@@ -32,7 +32,7 @@ struct MxArgs {
   uint32_t* faults;        // with ids
   int32_t zero_dropped;    // rows of dropped routes are written (as zeros)
   // otherwise the grouping: slot records of the experts, tiles of routes
-  int32_t tile_rows;       // most routes of a list tile (64 or 128)
+  int32_t tile_rows;       // most routes of a list tile (16 by slots, 64 or 128)
   int64_t max_tiles;       // bounds of the lists
   int32_t max_slots;
   const int32_t* tiles;    // [n_tiles][2] (expert, first place in sorted)

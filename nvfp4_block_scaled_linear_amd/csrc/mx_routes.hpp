@@ -57,8 +57,9 @@ __device__ __forceinline__ void clear_route(const MxArgs& a, int64_t r) {
 
 // The output rows of dropped routes become zeros, each by one wave, shared out over the launch:
 // batches are padded with routes that no expert takes. With half of 512 x top-4 routes like
-// that and 2048 columns of fp32, the product takes 42 us; with a lane of the grouping's one
-// workgroup to a row it took 1114.
+// that and 2048 columns of fp32, K = 2048 and 32 experts, the product takes 41 us with BF16
+// activations and 24 with MXFP4 ones (43 and 26 where all are routed); with a lane of the
+// grouping's one workgroup to a row it took 1114.
 //
 // After a grouping, a wave looks at as many routes as make them go round.
 template <int SWIGLU>

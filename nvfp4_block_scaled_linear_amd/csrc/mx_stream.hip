@@ -18,12 +18,13 @@
 // Loads past the rows, past K and past a wave's run are out of range: every step issues the
 // same number, which is what the counted waits go by.
 //
-// 16 x 12288 x 4096 with BF16 activations takes 8.8 us (27 MB, 3.0 TB/s), 1 x 2048 x 2048 3.2,
-// 4 x 4096 x 4096 with MXFP4 ones 3.9. Of a layer of 128 experts, top-8, for 16 tokens, gate_up
-// (2048 -> 2 x 768) takes 36.6 us and down (768 -> 2048) 19.9: 3.7 and 3.4 TB/s of the routed
-// experts' weights, in thousands of workgroups that live a few microseconds each, much of that
-// the time to their first load. Rings of several column blocks per workgroup and prefetches into
-// L2 were slower.
+// With weights from HBM, 16 x 12288 x 4096 with BF16 activations takes 10.5 us (27 MB, 2.5 TB/s; a
+// plain read of the codes 5.6), 1 x 2048 x 2048 3.9, 4 x 4096 x 4096 with MXFP4 ones 4.7 (a plain
+// read 3.0); with weights that the last-level cache holds 8.8, 3.2 and 3.9. Of a layer of 128
+// experts, top-8, for 16 tokens, gate_up (2048 -> 2 x 768) takes 36.4 us and down (768 -> 2048)
+// 19.7: 3.7 and 3.4 TB/s of the routed experts' weights, in thousands of workgroups that live a
+// few microseconds each, much of that the time to their first load. Rings of several column blocks
+// per workgroup and prefetches into L2 were slower.
 #include "mx_device.hpp"
 #include "mx_kernels.hpp"
 #include "mx_routes.hpp"
@@ -521,6 +522,11 @@ hipError_t launch_dense(const MxArgs& a, hipStream_t stream) {
   // So that a CU has about one workgroup: 16 x 12288 x 4096 takes 8.9 us with 48 weight rows
   // (256 workgroups), 11.2 with 16 (768, each loading the activations for itself).
   const int64_t nt = (a.N + 16 * 256 - 1) / (16 * 256);
+  //
+  // Steps in the ring (U), weights from HBM: BF16, 16 x 12288 x 4096 takes 10.7 us with 2, 10.8
+  // with 3, 11.4 with 4, K = 14336 and N = 4096 15.8, 16.8, 17.0. MXFP4, 4 x 4096 x 4096 takes
+  // 5.6, 4.8 and 4.7; where there are more rows of weight the fewer win again (12288: 9.4, 9.8,
+  // 10.0).
   if (nt <= 1) return launch_rows<ACT, XR, 1, 4, U>(a, stream);
   if (nt <= 2) return launch_rows<ACT, XR, 2, 4, U>(a, stream);
   return launch_rows<ACT, XR, 3, 4, U>(a, stream);

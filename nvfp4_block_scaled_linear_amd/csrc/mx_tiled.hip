@@ -19,12 +19,13 @@
 //    it stores 16 bytes at a time and holds a block's half or quarter when SwiGLU's result is
 //    quantized.
 //
-// 8192 x 14336 x 4096 with MXFP4 activations takes 259 us (3.7 PFLOP/s; the matrix cores are busy
-// 47 % of the time, the rest is loads from beyond L2, LDS reads and the stores of 235 MB),
-// 2048 x 14336 x 4096 with BF16 ones 196 to 205 (58 %; 448 tiles on 256 CUs leave an eighth of the
-// launch idle, and decoding takes VALU time). 512 x 4096 x 4096 MXFP4 takes 12.7. A prompt's
-// layer of 128 experts, 32768 routes, spends 129 us in gate_up (2048 -> 2 x 768) and 121 in down
-// (768 -> 2048, three stages and then 268 MB of fp32 rows).
+// 8192 x 14336 x 4096 with MXFP4 activations takes 251 to 259 us (3.7 PFLOP/s; the matrix cores are
+// busy 45 % of the time, the rest is loads from beyond L2, LDS reads and the stores of 235 MB),
+// 2048 x 14336 x 4096 with BF16 ones 195 to 205 (58 %; 448 tiles on 256 CUs leave an eighth of the
+// launch idle, and decoding takes VALU time). 512 x 4096 x 4096 MXFP4 takes 14.0 with its weight
+// from HBM, 12.7 otherwise. A prompt's layer of 128 experts, 32768 routes, spends 129 us in gate_up
+// (2048 -> 2 x 768; matrix cores 23 %) and 120 in down (768 -> 2048, three stages and then 268 MB
+// of fp32 rows; 12 %), with BF16 activations 234 and 216 (45 and 26 %).
 #include <type_traits>
 
 #include "mx_device.hpp"
