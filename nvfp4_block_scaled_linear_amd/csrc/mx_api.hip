@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "mx_kernels.hpp"
+#include "mx_plan.hpp"
 
 using namespace nvfp4;
 
@@ -79,66 +80,15 @@ bool streams(int32_t act_kind, int64_t M, int64_t N) {
   return M <= 32 || (M + 63) / 64 * ((N + 31) / 32) <= (act_kind == MXFP4_ACT_BF16 ? 550 : 300);
 }
 
-// How the grouped call goes about R = T * top_k routes. It depends on nothing else, so that
-// both calls of a layer agree on the workspace's grouping.
-//  - scan: few routes; each workgroup looks for its expert in topk_ids and nothing is grouped.
-//  - slots: less than kTiledRoutes routes per active expert on average; the weight is
-//    streamed for up to 16 routes, experts with more have the rest in the list of tiles.
-//  - tiles of up to 64 or 128 routes of an expert for more.
-// 32 experts, top-4, 2048 x 2048: 64 tokens take 21.0 us by slots and 28.3 in tiles, 96 26.0 and
-// 28.4, 128 30.6 and 28.8, 256 45.0 and 31.2 (MXFP4 activations 18.1 and 22.0, 24.5 and 22.3,
-// 29.1 and 22.6, 40.6 and 23.8). 256 tokens take 31.3 in tiles of 64 and 38.1 in tiles of 128,
-// 512 tokens 41.7 and 41.5 (MXFP4 23.7 and 24.0, 32.5 and 27.5). Without the scan, a layer of
-// 128 experts, top-8, takes 21.3 us for one token and 64.3 for 16 against 17.3 and 62.0.
+// Routes per active expert from which the grouped call works in tiles, and in tiles of 128
+// routes (see RoutePlan). 32 experts, top-4, 2048 x 2048: 64 tokens take 21.0 us by slots and
+// 28.3 in tiles, 96 26.0 and 28.4, 128 30.6 and 28.8, 256 45.0 and 31.2 (MXFP4 activations 18.1
+// and 22.0, 24.5 and 22.3, 29.1 and 22.6, 40.6 and 23.8). 256 tokens take 31.3 in tiles of 64 and
+// 38.1 in tiles of 128, 512 tokens 41.7 and 41.5 (MXFP4 23.7 and 24.0, 32.5 and 27.5). Without the
+// scan, a layer of 128 experts, top-8, takes 21.3 us for one token and 64.3 for 16 against 17.3
+// and 62.0.
 constexpr int64_t kTiledRoutes = 16;
 constexpr int64_t kTile128Routes = 64;
-
-struct Plan {
-  bool scan, slots;
-  int tile_rows, main_rows;
-  int64_t max_tiles;
-};
-
-Plan plan_of(int64_t T, int top_k, int E) {
-  const int64_t R = T * top_k, active = R < E ? R : E;
-  if (R < kTiledRoutes * active) {
-    // an expert has at most T routes; past its first 16, c routes make at most c / 16 tiles
-    if (R <= mx_scan_routes()) return {true, false, 0, 0, 0};
-    return {false, true, kMxSlotRoutes, kMxSlotRoutes, T > kMxSlotRoutes ? R / kMxSlotRoutes : 0};
-  }
-  const int rows = R < kTile128Routes * active ? 64 : 128;
-  return {false, false, rows, 0, R / rows + active};  // one partial tile per expert
-}
-
-// grouped-call workspace: 256-byte aligned regions, those of the grouping first and the same
-// in every output form
-struct Layout {
-  size_t offsets, active, n_active, route_expert, sorted, slots, tiles, n_tiles, chunks, rows, total;
-};
-
-size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
-
-Layout layout_of(const Plan& p, int64_t T, int top_k, int E, int64_t N, int32_t out_mode) {
-  Layout L{};
-  const int64_t R = T * top_k, active = R < E ? R : E;
-  size_t o = 256;  // never empty
-  const auto region = [&o](int64_t ints) { const size_t at = o; o = up256(o + 4 * (size_t)ints); return at; };
-  if (!p.scan) {
-    L.offsets = region(E + 1);
-    L.active = region(E);
-    L.n_active = region(1);
-    L.route_expert = region(R);
-    L.sorted = region(R);
-    L.slots = region(kSlotInts * active);
-    L.tiles = region(2 * p.max_tiles);
-    L.n_tiles = region(1);
-    L.chunks = region(route_chunk_ints(T, top_k, E));
-  }
-  L.rows = o;
-  if (out_mode == MXFP4_OUT_COMBINE) region(R * N);
-  L.total = o;
-  return L;
-}
 
 }  // namespace
 
@@ -226,8 +176,8 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
   if (out_mode == MXFP4_OUT_SWIGLU_BF16 && N % 2 != 0) return NVFP4_ERR_SHAPE;
   if (out_mode == MXFP4_OUT_SWIGLU_MXFP4 && N % 64 != 0) return NVFP4_ERR_SHAPE;
   if (!fits(N, K / 2)) return NVFP4_ERR_SHAPE;
-  const Plan plan = plan_of(T, top_k, num_experts);
-  const Layout L = layout_of(plan, T, top_k, num_experts, N, out_mode);
+  const RoutePlan plan = plan_routes(T, top_k, num_experts, kTiledRoutes, kTile128Routes);
+  const RouteLayout L = layout_routes(plan, T, top_k, num_experts, out_mode == MXFP4_OUT_COMBINE ? 4 * (size_t)N : 0);
   if (!workspace) {
     *workspace_bytes = L.total;
     return NVFP4_OK;
@@ -253,9 +203,7 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
                                     (int64_t)num_experts * N * (K / 32), faults, s);
     if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
   }
-  char* base = static_cast<char*>(workspace);
-  const auto ints = [base](size_t at) { return reinterpret_cast<int32_t*>(base + at); };
-  float* rows = reinterpret_cast<float*>(base + L.rows);
+  float* rows = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.rows);
   MxArgs a{};
   a.x = x; a.x_scales = x_scales; a.ldx = ldx;
   a.w_codes = w_codes; a.w_scales = w_scales;
@@ -269,34 +217,8 @@ nvfp4_status mxfp4_grouped_linear(int32_t act_kind, const void* x, const uint8_t
     a.y = rows;
     a.y_type = MXFP4_F32;
   }
-  hipError_t e = hipSuccess;
-  if (plan.scan) {
-    a.ids = topk_ids;
-    a.faults = reuse ? nullptr : faults;  // reported by the earlier call
-  } else {
-    RouteWorkspace ws{};
-    ws.offsets = ints(L.offsets);
-    ws.active = ints(L.active);
-    ws.n_active = ints(L.n_active);
-    ws.route_expert = ints(L.route_expert);
-    ws.sorted = ints(L.sorted);
-    ws.slots = ints(L.slots);
-    ws.max_slots = (int32_t)active;
-    ws.tiles = ints(L.tiles);
-    ws.n_tiles = ints(L.n_tiles);
-    ws.chunk_counts = ints(L.chunks);
-    ws.tile_rows = plan.tile_rows;
-    ws.main_rows = plan.main_rows;
-    if (!reuse) {
-      e = R <= kMxGroupRoutes
-              ? launch_mx_group(topk_ids, R, top_k, num_experts, ws, faults, s)
-              : launch_route_sort(topk_ids, T, top_k, num_experts, ws, faults, nullptr, 0, s);
-      if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
-    }
-    a.tile_rows = plan.tile_rows; a.max_tiles = plan.max_tiles; a.max_slots = ws.max_slots;
-    a.tiles = ws.tiles; a.n_tiles = ws.n_tiles; a.offsets = ws.offsets; a.sorted = ws.sorted;
-    a.slots = ws.slots; a.route_expert = ws.route_expert;
-  }
+  hipError_t e = prepare_routes(a, plan, L, workspace, topk_ids, T, reuse, faults, s);
+  if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
   e = plan.scan || plan.slots ? launch_mx_stream(a, act_kind, (R + active - 1) / active, s)
                               : launch_mx_tiled(a, act_kind, s);
   if (e != hipSuccess) return NVFP4_ERR_LAUNCH;

@@ -58,9 +58,9 @@ hipError_t launch_mx_tiled(const MxArgs& a, int act_kind, hipStream_t stream);
 // the weight streamed (mx_stream.hip) for about `rows` activation rows per weight (dense: M of
 // them), the grouped form by ids or by slots
 hipError_t launch_mx_stream(const MxArgs& a, int act_kind, int64_t rows, hipStream_t stream);
-// most routes in all that the form by ids takes, and the routes of a slot or a list tile of
-// the other
-int64_t mx_scan_routes();
+// most routes in all that the form by ids takes (four per lane), and the routes of a slot or a
+// list tile of the other
+constexpr int kScanRoutes = 256;
 constexpr int kMxSlotRoutes = 16;
 
 // groups up to kMxGroupRoutes routes; what launch_route_sort writes

@@ -157,117 +157,6 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
   wait_loads<0>();
 }
 
-// How a grouped workgroup finds its expert and the routes of it
-enum Mode {
-  kDense,
-  kByExpert,  // few routes in all: the workgroup looks for its routes in topk_ids
-  kBySlot     // from the grouping: a slot record's first kMxSlotRoutes routes, or a list tile
-};
-constexpr int kScanRoutes = 256;  // kByExpert: routes in all, four per lane
-
-// kByExpert: the workgroup groups of R routes. A group takes at most kMxSlotRoutes routes of an
-// expert, as a slot does, so that an expert that many tokens pick is spread over groups. With
-// fewer routes than experts the groups are the routes, and those whose place among their expert's
-// is a multiple of kMxSlotRoutes have work. Otherwise they are the experts' first routes, and as
-// many groups behind them as there can be runs of further ones (an expert has at most a route of
-// each token; past its first kMxSlotRoutes, c routes make at most c / kMxSlotRoutes runs).
-// A layer of 128 experts, 2048 / 768, BF16, takes 46 us for 256 tokens that all pick one expert, 75
-// for 64 tokens x top-4 that share one; in one workgroup a column block these were 276 and 119.
-// Tokens that pick evenly take what they took (one token 14.9 us, 16 46.5).
-__host__ __device__ inline int64_t scan_groups(int64_t R, int top_k, int E) {
-  return R < E ? R : E + (R / top_k > kMxSlotRoutes ? R / kMxSlotRoutes : 0);
-}
-
-// The expert and the first place of the run-th of the runs of routes that go past the experts'
-// first ones; false when there are fewer. By all of a workgroup, with R >= E and E ints of LDS.
-// (Routes that repeat an id within a token are counted: a run may turn out empty.)
-__device__ __forceinline__ bool further_run(const int32_t* ids, int R, int E, int run, int32_t* cnt,
-                                            int* expert, int* begin) {
-  const int lane = threadIdx.x & 63;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
-  __syncthreads();
-  for (int r = threadIdx.x; r < R; r += blockDim.x) {
-    const int32_t e = ids[r];
-    if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
-  }
-  __syncthreads();
-  bool found = false;
-  int before = 0;  // runs of the experts so far
-#pragma unroll
-  for (int i = 0; i < kScanRoutes / 64; i++) {
-    const int e = 64 * i + lane, c = e < E ? cnt[e] : 0;
-    const int own = c > 0 ? (c - 1) / kMxSlotRoutes : 0;
-    int upto = own;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(upto, d, 64);
-      if (lane >= d) upto += v;
-    }
-    const uint64_t hit = __ballot(run < before + upto && run >= before + upto - own);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      *expert = 64 * i + l;
-      *begin = kMxSlotRoutes * (1 + run - (before + __builtin_amdgcn_readlane(upto - own, l)));
-      found = true;
-    }
-    before += __builtin_amdgcn_readlane(upto, 63);
-  }
-  __syncthreads();  // the counters' LDS is used again
-  return found;
-}
-
-// The expert of workgroup group `group`, the bits of the routes 64 * i + lane that it keeps (those
-// that hold it and are not a repeat of it within their token; top_k <= 64: the token starts in
-// this group of 64 or the last), and the places [*begin, *end) among them that are the group's;
-// returns whether there are any.
-__device__ __forceinline__ bool scan_routes(const int32_t* ids, int R, int top_k, int E, int group,
-                                            int32_t* lds, int* expert, int* begin, int* end,
-                                            uint64_t (&kept)[kScanRoutes / 64]) {
-  const int lane = threadIdx.x & 63;
-  int e = group;
-  *begin = 0;
-  int32_t id[kScanRoutes / 64];
-#pragma unroll
-  for (int i = 0; i < kScanRoutes / 64; i++) id[i] = 64 * i + lane < R ? ids[64 * i + lane] : -1;
-  if (__builtin_expect(R >= E && group >= E, 0) && !further_run(ids, R, E, group - E, lds, &e, begin)) return false;
-  if (R < E) {
-#pragma unroll
-    for (int i = 0; i < kScanRoutes / 64; i++)
-      if (i == group / 64) e = __builtin_amdgcn_readlane(id[i], group % 64);
-    if (e < 0 || e >= E) return false;
-  }
-  *expert = e;
-  uint64_t last = 0u;
-  int count = 0, held = 0;  // routes kept, and with repeats
-#pragma unroll
-  for (int i = 0; i < kScanRoutes / 64; i++) {
-    const uint64_t m = __ballot(id[i] == e);
-    held += __builtin_popcountll(m);
-    kept[i] = m;
-    if (__builtin_popcountll(m) + (last != 0u) > 1) {  // there may be repeats
-      const int before = (64 * i + lane) % top_k;      // routes of the token before this one
-      // bit 63: the route before this one, bit 62 the one before that, ...
-      const uint64_t window = (lane ? m << (64 - lane) : 0u) | last >> lane;
-      const bool repeat = before && (window >> (64 - before)) != 0u;
-      kept[i] = __ballot(id[i] == e && !repeat);
-    }
-    last = m;
-    count += __builtin_popcountll(kept[i]);
-  }
-  if (R < E && held > 1) {  // this route's place, if it is kept (of one route there is no question)
-    bool mine = false;
-#pragma unroll
-    for (int i = 0; i < kScanRoutes / 64; i++) {
-      const uint64_t below = i < group / 64 ? ~0ull : i == group / 64 ? (1ull << group % 64) - 1 : 0ull;
-      *begin += __builtin_popcountll(kept[i] & below);
-      mine = mine || (i == group / 64 && (kept[i] >> group % 64 & 1));
-    }
-    if (!mine || *begin % kMxSlotRoutes != 0) return false;
-  }
-  *end = count - *begin < kMxSlotRoutes ? count : *begin + kMxSlotRoutes;
-  return *begin < *end;
-}
-
 template <class C, int MODE, int SWIGLU>
 __global__ __launch_bounds__(64 * C::W) void mx_stream(MxArgs a) {
   constexpr bool GROUPED = MODE != kDense;
@@ -553,8 +442,6 @@ hipError_t launch_act(const MxArgs& a, int64_t rows, hipStream_t stream) {
 }
 
 }  // namespace
-
-int64_t mx_scan_routes() { return kScanRoutes; }
 
 hipError_t launch_mx_stream(const MxArgs& a, int act_kind, int64_t rows, hipStream_t stream) {
   return act_kind == MXFP4_ACT_BF16 ? launch_act<MXFP4_ACT_BF16>(a, rows, stream)
