@@ -38,3 +38,13 @@ from ._mx import (  # noqa: F401
     mxfp4_linear,
     mxfp4_quantize,
 )
+from ._fp8 import (  # noqa: F401
+    FP8_EXPORTS,
+    OUT_SWIGLU_FP8,
+    fp8_dequantize,
+    fp8_grouped_linear,
+    fp8_grouped_workspace_size,
+    fp8_linear,
+    fp8_quantize,
+    moe_route,
+)

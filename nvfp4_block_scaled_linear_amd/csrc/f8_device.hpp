@@ -1,0 +1,60 @@
+// Device helpers of the FP8 kernels: E4M3 decode and encode, MFMA over a block of 128.
+#pragma once
+
+#include "fp8.h"
+#include "mx_device.hpp"
+
+namespace nvfp4 {
+
+constexpr float kF8Top = 448.0f;  // E4M3's largest value
+
+// MFMA over 128 k of E4M3 rows: lane l holds 32 codes of row l % 16 on either side, the same k on
+// both; result C[4 * (l / 16) + r][l % 16]. (Constant zeros for the block scales make it the
+// instruction without them.)
+//
+// The instruction sums less exactly than fp32. Of the products of eight consecutive k of a lane it
+// drops what lies below 2^-13 of the largest one's power of two (measured; the sums of eights
+// are added as in fp32; the older 16x16x32 form does the same), at most 7 * 2^-13 of that
+// product, and about 3e-5 of a result by the 2-norm with unit normal activations, loud channels
+// among them. BF16 results are rounded by 2^-9 of themselves, and E4M3 activations by 2^-4. Where
+// fp32 is asked for, codes are decoded to BF16, whose MFMA sums in fp32, at half the rate.
+__device__ __forceinline__ f32x4 mfma_f8(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x4 c) {
+  const i32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+  const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// 8 codes (two dwords, k ascending) -> 8 BF16, exact
+__device__ __forceinline__ u32x4 f8_decode8(uint32_t lo, uint32_t hi) {
+  u32x4 r;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, 0));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, 1));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, 0));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, 1));
+  return r;
+}
+
+// Four values of magnitude up to 448 -> their codes, nearest, ties to even (v_cvt_pk_fp8_f32)
+__device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+}
+
+// The scale of a block whose largest magnitude is amax (finite).
+template <int RULE>
+__device__ __forceinline__ float f8_scale(float amax) {
+  const float s = amax / kF8Top;
+  if (RULE == FP8_SCALE_F32) return s;
+  const uint32_t u = __float_as_uint(s);
+  if (u <= 1u) return s;
+  // a subnormal s is an integer times 2^-149; 2^23 of those are the least normal number
+  return __uint_as_float(u < 0x800000u ? 1u << (32 - __builtin_clz(u - 1)) : (u + 0x7FFFFFu) & 0xFF800000u);
+}
+
+// x / s for the encoder: +-0 where s is 0, and no more than 448
+__device__ __forceinline__ float f8_ratio(float x, float s) {
+  const float q = s == 0.0f ? __builtin_copysignf(0.0f, x) : x / s;
+  return __builtin_fminf(__builtin_fmaxf(q, -kF8Top), kF8Top);
+}
+
+}  // namespace nvfp4
