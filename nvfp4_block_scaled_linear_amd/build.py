@@ -24,7 +24,7 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 # scaled MFMAs in the accumulation-register form get their accumulators copied around in
 # every step.
 _VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-EXTRA = {f: _VGPR_FORM for f in ("stream.hip", "mx_stream.hip", "mx_tiled.hip", "f8_stream.hip")}
+EXTRA = {f: _VGPR_FORM for f in ("stream.hip", "mx_stream.hip", "mx_tiled.hip", "f8_stream.hip", "f8_tiled.hip")}
 
 
 def sources() -> list[str]:

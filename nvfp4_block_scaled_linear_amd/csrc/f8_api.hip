@@ -78,10 +78,15 @@ int kernel_kind(int32_t act_kind, int32_t y_type) {
 
 int64_t x_pitch(int32_t act_kind, int64_t ldx) { return act_kind == FP8_ACT_FP8 ? ldx : ldx * 2; }
 
+// Whether a dense product streams the weight or takes LDS tiles.
+bool streams(int32_t kind, int64_t M, int64_t N) {
+  return M <= 32 || (M + 63) / 64 * ((N + 31) / 32) <= 300;
+}
+
 // Routes per active expert from which the grouped call works in tiles, and in tiles of 128
 // routes (see RoutePlan).
-constexpr int64_t kTiledRoutes = (int64_t)1 << 40;
-constexpr int64_t kTile128Routes = (int64_t)1 << 40;
+constexpr int64_t kTiledRoutes = 16;
+constexpr int64_t kTile128Routes = 64;
 
 }  // namespace
 
@@ -139,7 +144,8 @@ nvfp4_status fp8_linear(int32_t act_kind, const void* x, const float* x_scales, 
   a.w_codes = w_codes; a.w_scales = w_scales;
   a.M = a.x_rows = M; a.N = N; a.K = K;
   a.y = y; a.ldy = ldy; a.y_type = y_type;
-  return launch_status(launch_f8_stream(a, kernel_kind(act_kind, y_type), M, s));
+  const int kind = kernel_kind(act_kind, y_type);
+  return launch_status(streams(kind, M, N) ? launch_f8_stream(a, kind, M, s) : launch_f8_tiled(a, kind, s));
 }
 
 nvfp4_status fp8_grouped_linear(int32_t act_kind, const void* x, const float* x_scales,
@@ -204,7 +210,9 @@ nvfp4_status fp8_grouped_linear(int32_t act_kind, const void* x, const float* x_
   a.swiglu = swiglu ? FP8_OUT_SWIGLU_BF16 : 0;
   a.zero_dropped = !combine;
   hipError_t e = prepare_routes(a, plan, L, workspace, topk_ids, T, reuse, faults, s);
-  if (e == hipSuccess) e = launch_f8_stream(a, kernel_kind(act_kind, y_type), (R + active - 1) / active, s);
+  const int kind = kernel_kind(act_kind, y_type);
+  if (e == hipSuccess)
+    e = plan.scan || plan.slots ? launch_f8_stream(a, kind, (R + active - 1) / active, s) : launch_f8_tiled(a, kind, s);
   if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
   if (combine)
     e = launch_mx_combine(static_cast<float*>(rows), N, topk_ids, topk_w, T, top_k, num_experts, N, y_type, y, N, s);

@@ -34,6 +34,14 @@ __device__ __forceinline__ u32x4 f8_decode8(uint32_t lo, uint32_t hi) {
   return r;
 }
 
+// 32 codes to BF16, eight k to a register group
+__device__ __forceinline__ void f8_decode32(u32x4 a, u32x4 b, u32x4 (&f)[4]) {
+  f[0] = f8_decode8(a[0], a[1]);
+  f[1] = f8_decode8(a[2], a[3]);
+  f[2] = f8_decode8(b[0], b[1]);
+  f[3] = f8_decode8(b[2], b[3]);
+}
+
 // Four values of magnitude up to 448 -> their codes, nearest, ties to even (v_cvt_pk_fp8_f32)
 __device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d) {
   const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);

@@ -59,6 +59,8 @@ hipError_t launch_f8_dequantize(const uint8_t* codes, const float* scales, int64
                                 int block_rows, int y_type, void* y, int64_t ldy,
                                 hipStream_t stream);
 
+// LDS tiles (f8_tiled.hip): dense, or the grouping's list of tiles of tile_rows routes
+hipError_t launch_f8_tiled(const F8Args& a, int act_kind, hipStream_t stream);
 // the weight streamed (f8_stream.hip) for about `rows` activation rows per weight (dense: M of
 // them), the grouped form by ids or by slots
 hipError_t launch_f8_stream(const F8Args& a, int act_kind, int64_t rows, hipStream_t stream);

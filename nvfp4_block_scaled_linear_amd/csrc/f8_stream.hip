@@ -44,14 +44,6 @@ struct Cfg {
 // slot s ^ row % 16 holds this piece: those that lanes g = 0..3 read together are neighbours.
 __device__ __forceinline__ int bf16_piece(int s) { return (s & 3) << 1 | ((s >> 2) & 1) | (s >> 3) << 3; }
 
-// 32 codes to BF16, eight k to a register group
-__device__ __forceinline__ void decode32(u32x4 a, u32x4 b, u32x4 (&f)[4]) {
-  f[0] = f8_decode8(a[0], a[1]);
-  f[1] = f8_decode8(a[2], a[3]);
-  f[2] = f8_decode8(b[0], b[1]);
-  f[3] = f8_decode8(b[2], b[3]);
-}
-
 struct Operands {
   u32x4 w, x, xs;  // descriptors
 };
@@ -120,7 +112,7 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
           xf[x][0] = x0;
           xf[x][1] = x1;
         } else {
-          decode32(x0, x1, xf[x]);
+          f8_decode32(x0, x1, xf[x]);
         }
       } else {
         // rows past the loaded ones read others' values, into columns that nobody stores
@@ -135,7 +127,7 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
       const u32x4 w0 = piece(b + C::W0, 16 * t + c, g), w1 = piece(b + C::W0, 16 * t + c, 4 + g);
       const float sw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w_scale[t]), sl));
       u32x4 wf[4];
-      if constexpr (!C::FAST) decode32(w0, w1, wf);
+      if constexpr (!C::FAST) f8_decode32(w0, w1, wf);
 #pragma unroll
       for (int x = 0; x < C::TM; x++) {
         f32x4 p = {0.f, 0.f, 0.f, 0.f};
