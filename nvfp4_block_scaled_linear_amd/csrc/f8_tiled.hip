@@ -40,8 +40,9 @@ struct Shape {
   static constexpr int SK = F8 ? 128 : 64;  // k of a stage
   static constexpr int XB = 128, WB = SK;   // bytes of a row per stage
   static constexpr int NX = BM * XB / (16 * T), NW = BN * WB / (16 * T);
+  static constexpr int RX = 16 * T / XB, RW = 16 * T / WB;  // rows of a load
   // scales of activation rows: one load of a window in four stages, out of range in the others
-  static constexpr int NS = F8 ? (BM + T - 1) / T : 0, WS = 4;
+  static constexpr int NS = F8 ? 1 : 0, WS = 4;
   static constexpr int LOADS = NX + NW + NS;
   static constexpr int X0 = 0, W0 = BM * XB, STAGE = W0 + BN * WB;
   static constexpr int WIN = F8 ? BM * 16 : 0;
@@ -50,7 +51,7 @@ struct Shape {
   static_assert(D - 1 <= WS, "a window is in use until it is overwritten");
   static_assert(16 * TW * 16 * 4 * WX * WW <= LDS, "the results' way out");
   static_assert(NX * 16 * T == BM * XB && NW * 16 * T == BN * WB, "whole loads only");
-  static_assert(LDS <= 160 * 1024, "LDS");
+  static_assert(LDS <= 160 * 1024 && BM <= T, "LDS");
   static_assert(TW % 4 == 0, "weight rows come in groups of 64 (SwiGLU: 32 + 32)");
 };
 
@@ -128,69 +129,73 @@ void f8_tiled(F8Args a, int gm, int vec) {
   const int64_t x_last = GROUPED ? a.x_rows : rows_m;
   const u32x4 xr = lds_load_rsrc(static_cast<const uint8_t*>(a.x) + (GROUPED ? 0 : m0 * xpitch),
                                  (x_last - 1) * xpitch + (int64_t)K * XE);
-  const u32x4 wr = lds_load_rsrc(wc + (SWIGLU ? 0 : n0 * K), (N - (SWIGLU ? 0 : n0)) * K);
-  // weight row of tile row t relative to that base, or -1
-  const auto w_row = [&](int t) -> int64_t {
-    if (!SWIGLU) return n0 + t < N ? t : -1;
-    const int u = t >= BC ? t - BC : t;
-    return n0 + u < half ? n0 + u + (t >= BC ? half : 0) : -1;
-  };
+  const int64_t w0 = SWIGLU ? 0 : n0;  // weight row that the offsets count from
+  const u32x4 wr = lds_load_rsrc(wc + w0 * K, (N - w0) * K);
   const auto w_swizzle = [](int t) { return ((t >> 1) & 1) | ((t / (4 * P)) & 3) << 1; };
 
-  // this lane's loads of stage 0, and the first k of each; a stage on, offsets grow by XB / WB
-  uint32_t xo[S::NX], wo[S::NW];
-  int xk[S::NX], wk[S::NW];
-#pragma unroll
-  for (int i = 0; i < S::NX; i++) {
-    const int p = i * S::T + tid, r = p >> 3;
-    int q = (p & 7) ^ ((r >> 1) & 7);
+  // This lane's loads of stage 0; a stage on, offsets grow by XB / WB. Load i is RX / RW rows
+  // further down than load 0 (a group's rows are gathered), at the same piece of its row, or where
+  // the swizzle goes by the load's parity at one of two. Rows past the tile's lie past the
+  // descriptor; gate and up (half % 128 == 0) end with a tile.
+  constexpr bool ODD = S::F8 && (S::RW / (4 * P) & 3) != 0;
+  static_assert(!ODD || (S::RW / (4 * P) & 3) == 2, "two places, 4 pieces apart");
+  int xk, wk[2];
+  uint32_t xo[GROUPED ? S::NX : 1], wo[2];
+  {
+    const int r = tid >> 3;
+    int q = (tid & 7) ^ ((r >> 1) & 7);
     if (!S::F8) q = (q & 3) << 1 | q >> 2;
-    xk[i] = q * (16 / XE);
-    xo[i] = r < rows_m ? (uint32_t)(x_row(r) * xpitch) + 16 * q : kOutOfRange;
-  }
+    xk = q * (16 / XE);
 #pragma unroll
-  for (int i = 0; i < S::NW; i++) {
-    const int p = i * S::T + tid;
+    for (int i = 0; i < (GROUPED ? S::NX : 1); i++) {
+      const int ri = i * S::RX + r;
+      xo[i] = ri < rows_m || !GROUPED ? (uint32_t)(x_row(ri) * xpitch) + 16 * q : kOutOfRange;
+    }
+  }
+  {
     int t, q;
     if (S::F8) {
-      t = p >> 3;
-      q = (p & 7) ^ w_swizzle(t);
-    } else {  // rows in the order of the MFMA's: row p / 4 is row p / 4 % 16 of 16-row tile p / 64
-      const int u = p >> 6, i16 = (p >> 2) & 15;
-      t = (u / P) * 16 * P + 4 * P * (i16 >> 2) + 4 * (u % P) + (i16 & 3);
-      q = (p & 3) ^ quarter_swizzle(i16);
+      t = tid >> 3;
+      q = (tid & 7) ^ w_swizzle(t);
+    } else {  // rows in the order of the MFMA's: tid / 4 is row tid / 4 % 16 of 16-row tile `wave`
+      const int r = (tid >> 2) & 15;
+      t = (wave / P) * 16 * P + 4 * P * (r >> 2) + 4 * (wave % P) + (r & 3);
+      q = (tid & 3) ^ quarter_swizzle(r);
     }
-    wk[i] = 16 * q;
-    const int64_t row = w_row(t);
-    wo[i] = row >= 0 ? (uint32_t)(row * K) + 16 * q : kOutOfRange;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int qi = ODD && i ? q ^ 4 : q;
+      wk[i] = 16 * qi;
+      wo[i] = (uint32_t)((n0 - w0 + t) * K) + 16 * qi;
+    }
   }
+  const uint32_t x_step = (uint32_t)(S::RX * xpitch), w_step = (uint32_t)(S::RW * K);
+  const uint32_t up = SWIGLU ? (uint32_t)((half - BC) * K) : 0u;  // from gate to up, past the tile's own rows
   u32x4 xsr = xr;
-  uint32_t so[S::NS ? S::NS : 1];
+  uint32_t so = kOutOfRange;
   if (S::F8) {
     xsr = lds_load_rsrc(a.x_scales + (GROUPED ? 0 : m0 * kb), 4 * x_last * kb);
-#pragma unroll
-    for (int i = 0; i < S::NS; i++) {
-      const int r = i * S::T + tid;
-      so[i] = r < rows_m ? (uint32_t)(4 * x_row(r) * kb) : kOutOfRange;
-    }
+    if (tid < S::BM && tid < rows_m) so = (uint32_t)(4 * x_row(tid) * kb);
   }
 
   const uint32_t lds0 = lds_address(smem);
   const auto issue = [&](int st, int buf) {
-    const uint32_t base = lds0 + buf * S::STAGE;
+    const uint32_t base = lds0 + buf * S::STAGE + wave * 1024;
     const int k0 = st * S::SK;
+    const bool x_in = k0 + xk < K;
 #pragma unroll
     for (int i = 0; i < S::NX; i++)
-      lds_load<16>(xr, k0 + xk[i] < K ? xo[i] + st * S::XB : kOutOfRange, base + S::X0 + (i * S::T + wave * 64) * 16);
+      lds_load<16>(xr, x_in ? xo[GROUPED ? i : 0] + (GROUPED ? 0 : i * x_step) + st * S::XB : kOutOfRange,
+                   base + S::X0 + i * S::T * 16);
+    const uint32_t w_at[2] = {k0 + wk[0] < K ? wo[0] + st * S::WB : kOutOfRange,
+                              k0 + wk[1] < K ? wo[1] + st * S::WB : kOutOfRange};
 #pragma unroll
     for (int i = 0; i < S::NW; i++)
-      lds_load<16>(wr, k0 + wk[i] < K ? wo[i] + st * S::WB : kOutOfRange, base + S::W0 + (i * S::T + wave * 64) * 16);
-#pragma unroll
-    for (int i = 0; i < S::NS; i++) {
-      const int r0 = i * S::T + wave * 64;
-      const bool now = st % S::WS == 0 && st < kb && r0 < S::BM;
-      lds_load<16>(xsr, now ? so[i] + 4 * st : kOutOfRange,
-                   now ? lds0 + S::WIN0 + st / S::WS % 2 * S::WIN + r0 * 16 : lds0 + S::SINK);
+      lds_load<16>(wr, w_at[ODD ? i & 1 : 0] + i * w_step + (i * S::RW >= BC ? up : 0), base + S::W0 + i * S::T * 16);
+    if (S::F8) {
+      const bool now = st % S::WS == 0 && st < kb && wave * 64 < S::BM;
+      lds_load<16>(xsr, now ? so + 4 * st : kOutOfRange,
+                   now ? lds0 + S::WIN0 + st / S::WS % 2 * S::WIN + wave * 1024 : lds0 + S::SINK);
     }
   };
 
@@ -211,22 +216,34 @@ void f8_tiled(F8Args a, int gm, int vec) {
     const int64_t n = SWIGLU ? n0 + ww * 16 * P + i * half : n0 + w_group(i * P);
     wsp[i] = ws + (n < N ? n >> 7 : 0) * kb;
   }
+  // where this lane reads: its pieces of an activation row and of a weight row (the second lies 64
+  // bytes on or back), and the row's scale
+  const int xrow = wx * S::TX * 16 + c;
+  const int x_at = S::X0 + xrow * 128 + ((g ^ ((xrow >> 1) & 7)) << 4);
+  const int wrow = w_local(0, c);
+  const int w_at = S::F8 ? S::W0 + wrow * 128 + ((g ^ w_swizzle(wrow)) << 4)
+                         : S::W0 + w_group(0) * 64 + 64 * c + ((g ^ quarter_swizzle(c)) << 4);
+  // from weight tile 0 to tile t
+  const auto w_off = [&](int t) {
+    return SWIGLU ? t / P * BC * S::WB + t % P * (S::F8 ? 4 * 128 : 1024) : S::F8 ? t * 4 * 128 : t * 1024;
+  };
+  static_assert(SWIGLU || GROUPS == 1, "");
 
   const int steps = (K + S::SK - 1) / S::SK;
 #pragma unroll
   for (int i = 0; i < S::D - 1; i++) issue(i, i);
   float w_scale[GROUPS];
-  const auto stage = [&](int st, int buf) {
+  int buf = 0;
+  for (int st = 0; st < steps; st++) {
     const int b = S::F8 ? st : st >> 1;  // block of scales
-    if ((b & 63) == 0 && (S::F8 || (st & 1) == 0)) {
+    if ((b & 63) == 0) {
 #pragma unroll
       for (int i = 0; i < GROUPS; i++) w_scale[i] = b + lane < kb ? wsp[i][b + lane] : 0.f;
     }
     wait_loads_barrier<(S::D - 2) * S::LOADS>();
     issue(st + S::D - 1, buf == 0 ? S::D - 1 : buf - 1);
-    const uint8_t* xs = smem + buf * S::STAGE + S::X0;
-    const uint8_t* wl = smem + buf * S::STAGE + S::W0;
-    const uint8_t* sl = smem + S::WIN0 + st / S::WS % 2 * S::WIN + st % S::WS * 4;
+    const uint8_t* const xl = smem + buf * S::STAGE + x_at;
+    const uint8_t* const wl = smem + buf * S::STAGE + w_at;
     float sw[GROUPS];
 #pragma unroll
     for (int i = 0; i < GROUPS; i++)
@@ -235,68 +252,80 @@ void f8_tiled(F8Args a, int gm, int vec) {
 #pragma unroll
       for (int i = 0; i < 4; i++) acc[t][x][i] = __builtin_fmaf(p[i], sc, acc[t][x][i]);
     };
+    const auto piece = [](const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); };
     if constexpr (S::F8) {
+      const uint8_t* const xl2 = smem + buf * S::STAGE + (x_at ^ 64);
+      const uint8_t* const wl2 = smem + buf * S::STAGE + (w_at ^ 64);
+      const uint8_t* const sl = smem + S::WIN0 + st / S::WS % 2 * S::WIN + st % S::WS * 4 + xrow * 16;
       u32x4 wf[S::TW][S::FAST ? 2 : 4];
 #pragma unroll
       for (int t = 0; t < S::TW; t++) {
-        const int r = w_local(t, c);
-        const u32x4 w0 = *reinterpret_cast<const u32x4*>(wl + r * 128 + ((g ^ w_swizzle(r)) << 4));
-        const u32x4 w1 = *reinterpret_cast<const u32x4*>(wl + r * 128 + (((4 + g) ^ w_swizzle(r)) << 4));
         if constexpr (S::FAST) {
-          wf[t][0] = w0;
-          wf[t][1] = w1;
+          wf[t][0] = piece(wl + w_off(t));
+          wf[t][1] = piece(wl2 + w_off(t));
         } else {
-          f8_decode32(w0, w1, wf[t]);
+          f8_decode32(piece(wl + w_off(t)), piece(wl2 + w_off(t)), wf[t]);
         }
       }
+      // The reads of row tile x + 1, the MFMAs of tile x and the FMAs of tile x - 1 go side by side.
+      u32x4 xq[2][2];
+      float sx[2];
+      f32x4 p[2][S::TW];
+      const auto read = [&](int x) {
+        xq[x & 1][0] = piece(xl + x * 2048);
+        xq[x & 1][1] = piece(xl2 + x * 2048);
+      };
+      read(0);
 #pragma unroll
-      for (int x = 0; x < S::TX; x++) {
-        const int r = (wx * S::TX + x) * 16 + c;
-        const u32x4 x0 = *reinterpret_cast<const u32x4*>(xs + r * 128 + ((g ^ ((r >> 1) & 7)) << 4));
-        const u32x4 x1 = *reinterpret_cast<const u32x4*>(xs + r * 128 + (((4 + g) ^ ((r >> 1) & 7)) << 4));
-        const float sx = *reinterpret_cast<const float*>(sl + r * 16);
-        u32x4 xf[4];
-        if constexpr (!S::FAST) f8_decode32(x0, x1, xf);
+      for (int x = 0; x <= S::TX; x++) {
+        if (x + 1 < S::TX) read(x + 1);
+        if (x < S::TX) {
+          sx[x & 1] = *reinterpret_cast<const float*>(sl + x * 256);
+          u32x4 xf[4];
+          if constexpr (!S::FAST) f8_decode32(xq[x & 1][0], xq[x & 1][1], xf);
 #pragma unroll
-        for (int t = 0; t < S::TW; t++) {
-          f32x4 p = {0.f, 0.f, 0.f, 0.f};
-          if constexpr (S::FAST) {
-            p = mfma_f8(wf[t][0], wf[t][1], x0, x1, p);
-          } else {
+          for (int t = 0; t < S::TW; t++) {
+            f32x4 q = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (S::FAST) {
+              q = mfma_f8(wf[t][0], wf[t][1], xq[x & 1][0], xq[x & 1][1], q);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; j++) p = mfma16(wf[t][j], xf[j], p);
+              for (int j = 0; j < 4; j++) q = mfma16(wf[t][j], xf[j], q);
+            }
+            p[x & 1][t] = q;
           }
-          add(t, x, p, sw[t / P] * sx);
         }
+        if (x > 0) {
+#pragma unroll
+          for (int t = 0; t < S::TW; t++) add(t, x - 1, p[(x - 1) & 1][t], sw[t / P] * sx[(x - 1) & 1]);
+        }
+        if constexpr (S::FAST) {
+#pragma unroll
+          for (int t = 0; t < S::TW; t++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // an MFMA
+            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);  // vector operations
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
+      const uint8_t* const xl2 = smem + buf * S::STAGE + (x_at ^ 64);
       u32x4 xf[S::TX][2];
 #pragma unroll
       for (int x = 0; x < S::TX; x++) {
-        const int r = (wx * S::TX + x) * 16 + c;
-#pragma unroll
-        for (int j = 0; j < 2; j++)
-          xf[x][j] = *reinterpret_cast<const u32x4*>(xs + r * 128 + (((g + 4 * j) ^ ((r >> 1) & 7)) << 4));
+        xf[x][0] = piece(xl + x * 2048);
+        xf[x][1] = piece(xl2 + x * 2048);
       }
 #pragma unroll
       for (int t = 0; t < S::TW; t++) {
-        // 16-row tile in the order of the loads
-        const int u = w_group(t) / 16 + t % P;
-        const u32x4 w = *reinterpret_cast<const u32x4*>(wl + u * 1024 + 64 * c + ((g ^ quarter_swizzle(c)) << 4));
-        const u32x4 w0 = f8_decode8(w[0], w[1]), w1 = f8_decode8(w[2], w[3]);
+        const u32x4 w = piece(wl + w_off(t));
+        const u32x4 f0 = f8_decode8(w[0], w[1]), f1 = f8_decode8(w[2], w[3]);
 #pragma unroll
         for (int x = 0; x < S::TX; x++)
-          add(t, x, mfma16(w1, xf[x][1], mfma16(w0, xf[x][0], f32x4{0.f, 0.f, 0.f, 0.f})), sw[t / P]);
+          add(t, x, mfma16(f1, xf[x][1], mfma16(f0, xf[x][0], f32x4{0.f, 0.f, 0.f, 0.f})), sw[t / P]);
       }
     }
-  };
-  // the ring's buffers are taken in turn, by a loop that is unrolled so that they are constants
-  for (int st0 = 0; st0 < steps; st0 += S::D) {
-#pragma unroll
-    for (int i = 0; i < S::D; i++) {
-      if (i && st0 + i >= steps) break;
-      stage(st0 + i, i);
-    }
+    buf = buf + 1 == S::D ? 0 : buf + 1;
   }
   wait_loads<0>();  // nothing writes LDS after the workgroup
 
@@ -376,7 +405,9 @@ hipError_t launch_act(const F8Args& a, hipStream_t stream) {
     return (a.tiles ? a.R / bm + active : (a.M + bm - 1) / bm) * ((cols + bc - 1) / bc);
   };
   const int64_t rows = !a.tiles ? a.M : a.tile_rows < grouped_rows(ACT) ? a.tile_rows : grouped_rows(ACT);
-  if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_shape<Shape<ACT, 256, 256, 2, 4, F8 ? 2 : 3>>(a, stream);
+  if constexpr (ACT != kF8Exact) {  // (whose decoded operands leave no registers for it)
+    if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_shape<Shape<ACT, 256, 256, 2, 4, F8 ? 2 : 3>>(a, stream);
+  }
   if (rows > 64 && tiles(128, 256) >= kFewTiles) return launch_shape<Shape<ACT, 128, 256, 2, 4, 3>>(a, stream);
   if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_shape<Shape<ACT, 128, 128, 2, 2, F8 ? 3 : 4>>(a, stream);
   if (tiles(64, 256) >= kFewTiles) return launch_shape<Shape<ACT, 64, 256, F8 ? 2 : 1, 4, 3>>(a, stream);
