@@ -13,8 +13,8 @@
 //    times both scales. (It is less exact than fp32: see mfma_f8.)
 //  - otherwise the lane decodes its 32 codes to BF16 (for results in fp32 those of FP8 activations
 //    too), four MFMAs over 32 k each from zero, whose result is added times the scales.
-// The 16 weight rows of an MFMA lie in one block of 128, so its scale is the same for a wave: lane
-// l of a wave holds those of the step that is l on, and they come from it as scalars.
+// The 16 weight rows of an MFMA lie in one block of 128, so its scale is the same for a wave: those
+// of 64 steps are loaded at once.
 // Loads past the rows, past K and past a wave's run are out of range: every step issues the
 // same number, which is what the counted waits go by.
 #include "f8_device.hpp"
@@ -34,7 +34,7 @@ struct Cfg {
   static constexpr int SX = F8 ? 1 : 0;              // loads of their scales
   static constexpr int LOADS = 2 * NT + XMAX + SX;
   static constexpr int W0 = 0, X0 = 2048 * NT, S0 = X0 + 1024 * XMAX, STEP = S0 + 256 * SX;
-  static constexpr int RING = STEP * U;     // of a wave
+  static constexpr int WS0 = STEP * U, RING = WS0 + 256 * NT;  // of a wave: steps, scales of the weight
   static constexpr int PART = 1024 * NT * TM;  // partial sums of a wave
   static constexpr int LDS = W * (RING > PART ? RING : PART);
   static_assert(NT <= 4 && TM <= 4 && LDS <= 160 * 1024, "");
@@ -45,16 +45,16 @@ struct Cfg {
 __device__ __forceinline__ int bf16_piece(int s) { return (s & 3) << 1 | ((s >> 2) & 1) | (s >> 3) << 3; }
 
 struct Operands {
-  u32x4 w, x, xs;  // descriptors
+  u32x4 w, ws, x, xs;  // descriptors
 };
 
-// One wave's run [s0, s1) of steps over the rows whose lanes' offsets are wo, xo, xso; ws: where
-// the scales of its weight tiles lie.
+// One wave's run [s0, s1) of steps over the rows whose lanes' offsets are wo, xo, xso; wso: where
+// its weight tiles' scales begin.
 template <class C>
 __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, const uint8_t* ring_p,
                                           int s0, int s1, int K, const uint32_t* wo,
                                           const uint32_t* xo, uint32_t xso,
-                                          const float* const (&ws)[C::NT],
+                                          const uint32_t (&wso)[C::NT],
                                           f32x4 (&acc)[C::NT][C::TM]) {
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const auto issue = [&](int s, int u) {
@@ -80,15 +80,21 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
     }
     if (C::F8) lds_load<4>(d.xs, in ? xso + 4 * s : kOutOfRange, base + C::S0);
   };
+  // the weight tiles' scales of 64 steps from s on
+  const auto load_scales = [&](int s) {
+#pragma unroll
+    for (int t = 0; t < C::NT; t++) lds_load<4>(d.ws, s + lane < s1 ? wso[t] + 4 * (s + lane) : kOutOfRange, ring + C::WS0 + 256 * t);
+  };
+  load_scales(s0);
 #pragma unroll
   for (int u = 0; u < C::U - 1; u++) issue(s0 + u, u);
-  float w_scale[C::NT];
   int u = 0;
   for (int s = s0; s < s1; s++) {
     const int sl = (s - s0) & 63;
-    if (sl == 0) {
-#pragma unroll
-      for (int t = 0; t < C::NT; t++) w_scale[t] = s + lane < s1 ? ws[t][s + lane] : 0.f;
+    if (sl == 0 && s > s0) {
+      wait_lds_reads();
+      load_scales(s);
+      wait_loads<0>();
     }
     wait_lds_reads();  // of the step whose bytes the next loads overwrite
     issue(s + C::U - 1, u == 0 ? C::U - 1 : u - 1);
@@ -125,7 +131,7 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
 #pragma unroll
     for (int t = 0; t < C::NT; t++) {
       const u32x4 w0 = piece(b + C::W0, 16 * t + c, g), w1 = piece(b + C::W0, 16 * t + c, 4 + g);
-      const float sw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w_scale[t]), sl));
+      const float sw = *reinterpret_cast<const float*>(ring_p + C::WS0 + 256 * t + 4 * sl);
       u32x4 wf[4];
       if constexpr (!C::FAST) f8_decode32(w0, w1, wf);
 #pragma unroll
@@ -205,6 +211,7 @@ __global__ __launch_bounds__(64 * C::W) void f8_stream(F8Args a) {
   Operands d;
   const int r0 = SWIGLU ? 0 : n0;  // weight row that the offsets count from
   d.w = lds_load_rsrc(wc + (int64_t)r0 * K, (int64_t)(N - r0) * K);
+  d.ws = lds_load_rsrc(wsc + (int64_t)(r0 >> 7) * kb, 4 * (int64_t)(((N + 127) >> 7) - (r0 >> 7)) * kb);
   const uint32_t xpitch = (uint32_t)a.ldx * (C::F8 ? 1 : 2);
   const int64_t x_rows = GROUPED ? a.x_rows : count;
   d.x = lds_load_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)row0 * xpitch,
@@ -215,12 +222,10 @@ __global__ __launch_bounds__(64 * C::W) void f8_stream(F8Args a) {
     const int n = n0 + 16 * (t % NO) + i;
     return n < cols ? n - r0 + (t >= NO ? half : 0) : -1;
   };
-  const float* ws[C::NT];
+  uint32_t wso[C::NT];
 #pragma unroll
-  for (int t = 0; t < C::NT; t++) {
-    const int n = n0 + 16 * (t % NO);  // a tile past the columns takes the first one's
-    ws[t] = wsc + (int64_t)(((n < cols ? n : 0) + (t >= NO ? half : 0)) >> 7) * kb;
-  }
+  for (int t = 0; t < C::NT; t++)  // (past the weight's rows it is out of range)
+    wso[t] = 4u * (uint32_t)((n0 + 16 * (t % NO) + (t >= NO ? half : 0) - (r0 & ~127)) >> 7) * (uint32_t)kb;
   uint32_t wo[2 * C::NT];
 #pragma unroll
   for (int i = 0; i < 2 * C::NT; i++) {
@@ -273,7 +278,7 @@ __global__ __launch_bounds__(64 * C::W) void f8_stream(F8Args a) {
     for (int t = 0; t < C::NT; t++)
 #pragma unroll
       for (int x = 0; x < C::TM; x++) acc[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (s0 < s1) run_steps<C>(d, ring, ring_p, s0, s1, K, wo, xo, xso, ws, acc);
+    if (s0 < s1) run_steps<C>(d, ring, ring_p, s0, s1, K, wo, xo, xso, wso, acc);
     // partial sums of this wave [NT][TM][64], in the bytes of its ring
     const auto part = [&](int w) { return reinterpret_cast<f32x4*>(smem + w * WAVE); };
 #pragma unroll
@@ -373,7 +378,7 @@ hipError_t launch_act(const F8Args& a, int64_t rows, hipStream_t stream) {
   if (rows <= 4) return launch_dense<ACT, F8 ? 16 : 4, F8 ? 3 : 2>(a, stream);
   if (rows <= 16) return launch_dense<ACT, 16, F8 ? 3 : 2>(a, stream);
   if (rows <= 32) return launch_rows<ACT, 32, 2, 4, 2>(a, stream);
-  return launch_rows<ACT, 64, 2, 4, 2>(a, stream);
+  return launch_rows<ACT, F8 ? 64 : 48, 2, 4, 2>(a, stream);
 }
 
 }  // namespace

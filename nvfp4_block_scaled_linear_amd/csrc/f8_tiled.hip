@@ -44,6 +44,8 @@ struct Shape {
   // scales of activation rows: one load of a window in four stages, out of range in the others
   static constexpr int NS = F8 ? 1 : 0, WS = 4;
   static constexpr int LOADS = NX + NW + NS;
+  static constexpr int KF = F8 && !FAST ? 4 : 2;              // register groups of a row's k
+  static constexpr int PER = (LOADS + TX / 2 - 1) / (TX / 2);  // loads of a step
   static constexpr int X0 = 0, W0 = BM * XB, STAGE = W0 + BN * WB;
   static constexpr int WIN = F8 ? BM * 16 : 0;
   static constexpr int WIN0 = D * STAGE, SINK = WIN0 + 2 * WIN;  // SINK: bytes that nobody reads
@@ -52,7 +54,7 @@ struct Shape {
   static_assert(16 * TW * 16 * 4 * WX * WW <= LDS, "the results' way out");
   static_assert(NX * 16 * T == BM * XB && NW * 16 * T == BN * WB, "whole loads only");
   static_assert(LDS <= 160 * 1024 && BM <= T, "LDS");
-  static_assert(TW % 4 == 0, "weight rows come in groups of 64 (SwiGLU: 32 + 32)");
+  static_assert(TX % 2 == 0 && TW % 4 == 0, "weight rows come in groups of 64 (SwiGLU: 32 + 32)");
 };
 
 // slot of piece q of a weight row of 64 bytes is q ^ quarter_swizzle(row)
@@ -179,20 +181,19 @@ void f8_tiled(F8Args a, int gm, int vec) {
   }
 
   const uint32_t lds0 = lds_address(smem);
-  const auto issue = [&](int st, int buf) {
-    const uint32_t base = lds0 + buf * S::STAGE + wave * 1024;
+  // the i-th load of stage st
+  const auto issue = [&](int st, int buf, int i) {
+    const uint32_t to = lds0 + buf * S::STAGE + wave * 1024;
     const int k0 = st * S::SK;
-    const bool x_in = k0 + xk < K;
-#pragma unroll
-    for (int i = 0; i < S::NX; i++)
-      lds_load<16>(xr, x_in ? xo[GROUPED ? i : 0] + (GROUPED ? 0 : i * x_step) + st * S::XB : kOutOfRange,
-                   base + S::X0 + i * S::T * 16);
-    const uint32_t w_at[2] = {k0 + wk[0] < K ? wo[0] + st * S::WB : kOutOfRange,
-                              k0 + wk[1] < K ? wo[1] + st * S::WB : kOutOfRange};
-#pragma unroll
-    for (int i = 0; i < S::NW; i++)
-      lds_load<16>(wr, w_at[ODD ? i & 1 : 0] + i * w_step + (i * S::RW >= BC ? up : 0), base + S::W0 + i * S::T * 16);
-    if (S::F8) {
+    if (i < S::NX) {
+      lds_load<16>(xr, k0 + xk < K ? xo[GROUPED ? i : 0] + (GROUPED ? 0 : i * x_step) + st * S::XB : kOutOfRange,
+                   to + S::X0 + i * S::T * 16);
+    } else if (i < S::NX + S::NW) {
+      i -= S::NX;
+      lds_load<16>(wr, (k0 + wk[ODD ? i & 1 : 0] < K ? wo[ODD ? i & 1 : 0] + st * S::WB : kOutOfRange) + i * w_step +
+                           (i * S::RW >= BC ? up : 0),
+                   to + S::W0 + i * S::T * 16);
+    } else {
       const bool now = st % S::WS == 0 && st < kb && wave * 64 < S::BM;
       lds_load<16>(xsr, now ? so + 4 * st : kOutOfRange,
                    now ? lds0 + S::WIN0 + st / S::WS % 2 * S::WIN + wave * 1024 : lds0 + S::SINK);
@@ -229,104 +230,129 @@ void f8_tiled(F8Args a, int gm, int vec) {
   };
   static_assert(SWIGLU || GROUPS == 1, "");
 
+  const auto piece = [](const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); };
+  u32x4 wf[S::TW][S::KF], xq[2][2];
+  float sx[2];
+  const auto read_w = [&](int buf) {
+    const uint8_t* const l = smem + buf * S::STAGE;
+#pragma unroll
+    for (int t = 0; t < S::TW; t++) {
+      const u32x4 w0 = piece(l + w_at + w_off(t));
+      if constexpr (!S::F8) {
+        wf[t][0] = f8_decode8(w0[0], w0[1]);
+        wf[t][1] = f8_decode8(w0[2], w0[3]);
+      } else {
+        const u32x4 w1 = piece(l + (w_at ^ 64) + w_off(t));
+        if constexpr (S::FAST) {
+          wf[t][0] = w0;
+          wf[t][1] = w1;
+        } else {
+          f8_decode32(w0, w1, wf[t]);
+        }
+      }
+    }
+  };
+  const auto read_x = [&](int st, int buf, int x) {
+    const uint8_t* const l = smem + buf * S::STAGE + x * 2048;
+    xq[x & 1][0] = piece(l + x_at);
+    xq[x & 1][1] = piece(l + (x_at ^ 64));
+    if (S::F8)
+      sx[x & 1] = *reinterpret_cast<const float*>(smem + S::WIN0 + st / S::WS % 2 * S::WIN + st % S::WS * 4 + xrow * 16 + x * 256);
+  };
+  // products of a row tile, and the scale of each group of weight rows that they are added with
+  f32x4 p[2][S::TW];
+  float sc[2][GROUPS];
+  const auto add = [&](int x) {
+#pragma unroll
+    for (int t = 0; t < S::TW; t++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) acc[t][x][i] = __builtin_fmaf(p[x & 1][t][i], sc[x & 1][t / P], acc[t][x][i]);
+  };
+#pragma unroll
+  for (int t = 0; t < S::TW; t++) p[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < GROUPS; i++) sc[1][i] = 0.f;
+
+  // this lane's scale of each group, of 64 blocks from b on; waited for by themselves, because a wait
+  // at their use would be for loads into LDS as well
+  float w_scale[GROUPS];
+  const auto load_scales = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < GROUPS; i++) w_scale[i] = b + lane < kb ? wsp[i][b + lane] : 0.f;
+  };
+  const auto wait_scales = [&] {
+#pragma unroll
+    for (int i = 0; i < GROUPS; i++) asm volatile("" : "+v"(w_scale[i]));
+  };
+  load_scales(0);
   const int steps = (K + S::SK - 1) / S::SK;
 #pragma unroll
-  for (int i = 0; i < S::D - 1; i++) issue(i, i);
-  float w_scale[GROUPS];
+  for (int s = 0; s < S::D - 1; s++)
+#pragma unroll
+    for (int i = 0; i < S::LOADS; i++) issue(s, s, i);
+  wait_loads_barrier<(S::D - 2) * S::LOADS>();
+  read_w(0);
+  read_x(0, 0, 0);
+  wait_scales();
   int buf = 0;
   for (int st = 0; st < steps; st++) {
     const int b = S::F8 ? st : st >> 1;  // block of scales
-    if ((b & 63) == 0) {
-#pragma unroll
-      for (int i = 0; i < GROUPS; i++) w_scale[i] = b + lane < kb ? wsp[i][b + lane] : 0.f;
+    if (st > 0 && st % (64 * 128 / S::SK) == 0) {
+      load_scales(b);
+      wait_scales();
     }
-    wait_loads_barrier<(S::D - 2) * S::LOADS>();
-    issue(st + S::D - 1, buf == 0 ? S::D - 1 : buf - 1);
-    const uint8_t* const xl = smem + buf * S::STAGE + x_at;
-    const uint8_t* const wl = smem + buf * S::STAGE + w_at;
+    const int next = buf + 1 == S::D ? 0 : buf + 1, free = buf == 0 ? S::D - 1 : buf - 1;
     float sw[GROUPS];
 #pragma unroll
     for (int i = 0; i < GROUPS; i++)
       sw[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w_scale[i]), b & 63));
-    const auto add = [&](int t, int x, f32x4 p, float sc) {
+    // Step x: the MFMAs of row tile x, the reads of tile x + 1, the FMAs of tile x - 1, and in the
+    // stage's first half the loads of the stage that is D - 1 on.
 #pragma unroll
-      for (int i = 0; i < 4; i++) acc[t][x][i] = __builtin_fmaf(p[i], sc, acc[t][x][i]);
-    };
-    const auto piece = [](const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); };
-    if constexpr (S::F8) {
-      const uint8_t* const xl2 = smem + buf * S::STAGE + (x_at ^ 64);
-      const uint8_t* const wl2 = smem + buf * S::STAGE + (w_at ^ 64);
-      const uint8_t* const sl = smem + S::WIN0 + st / S::WS % 2 * S::WIN + st % S::WS * 4 + xrow * 16;
-      u32x4 wf[S::TW][S::FAST ? 2 : 4];
+    for (int x = 0; x < S::TX; x++) {
+#pragma unroll
+      for (int i = x * S::PER; i < (x + 1) * S::PER && i < S::LOADS; i++) issue(st + S::D - 1, free, i);
+      u32x4 xf[S::KF];
+      if constexpr (S::F8 && !S::FAST) {
+        f8_decode32(xq[x & 1][0], xq[x & 1][1], xf);
+      } else {
+        xf[0] = xq[x & 1][0];
+        xf[1] = xq[x & 1][1];
+      }
+#pragma unroll
+      for (int i = 0; i < GROUPS; i++) sc[x & 1][i] = S::F8 ? sw[i] * sx[x & 1] : sw[i];
+      if (x + 1 < S::TX) read_x(st, buf, x + 1);
 #pragma unroll
       for (int t = 0; t < S::TW; t++) {
+        f32x4 q = {0.f, 0.f, 0.f, 0.f};
         if constexpr (S::FAST) {
-          wf[t][0] = piece(wl + w_off(t));
-          wf[t][1] = piece(wl2 + w_off(t));
+          q = mfma_f8(wf[t][0], wf[t][1], xf[0], xf[1], q);
         } else {
-          f8_decode32(piece(wl + w_off(t)), piece(wl2 + w_off(t)), wf[t]);
+#pragma unroll
+          for (int j = 0; j < S::KF; j++) q = mfma16(wf[t][j], xf[j], q);
         }
+        p[x & 1][t] = q;
       }
-      // The reads of row tile x + 1, the MFMAs of tile x and the FMAs of tile x - 1 go side by side.
-      u32x4 xq[2][2];
-      float sx[2];
-      f32x4 p[2][S::TW];
-      const auto read = [&](int x) {
-        xq[x & 1][0] = piece(xl + x * 2048);
-        xq[x & 1][1] = piece(xl2 + x * 2048);
-      };
-      read(0);
-#pragma unroll
-      for (int x = 0; x <= S::TX; x++) {
-        if (x + 1 < S::TX) read(x + 1);
-        if (x < S::TX) {
-          sx[x & 1] = *reinterpret_cast<const float*>(sl + x * 256);
-          u32x4 xf[4];
-          if constexpr (!S::FAST) f8_decode32(xq[x & 1][0], xq[x & 1][1], xf);
-#pragma unroll
-          for (int t = 0; t < S::TW; t++) {
-            f32x4 q = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (S::FAST) {
-              q = mfma_f8(wf[t][0], wf[t][1], xq[x & 1][0], xq[x & 1][1], q);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; j++) q = mfma16(wf[t][j], xf[j], q);
-            }
-            p[x & 1][t] = q;
-          }
-        }
-        if (x > 0) {
-#pragma unroll
-          for (int t = 0; t < S::TW; t++) add(t, x - 1, p[(x - 1) & 1][t], sw[t / P] * sx[(x - 1) & 1]);
-        }
-        if constexpr (S::FAST) {
-#pragma unroll
-          for (int t = 0; t < S::TW; t++) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // an MFMA
-            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);  // vector operations
-          }
-        }
+      if (x + 1 == S::TX) {
+        // the stage has been read, and the next one is there when all waves have come here
         __builtin_amdgcn_sched_barrier(0);
+        wait_loads_barrier<(S::D - 2) * S::LOADS>();
+        read_w(next);
+        read_x(st + 1, next, 0);
       }
-    } else {
-      const uint8_t* const xl2 = smem + buf * S::STAGE + (x_at ^ 64);
-      u32x4 xf[S::TX][2];
+      add(x > 0 ? x - 1 : S::TX - 1);
+      if (S::FAST && x + 1 < S::TX) {
 #pragma unroll
-      for (int x = 0; x < S::TX; x++) {
-        xf[x][0] = piece(xl + x * 2048);
-        xf[x][1] = piece(xl2 + x * 2048);
+        for (int t = 0; t < S::TW; t++) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // an MFMA
+          __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);  // vector operations
+        }
       }
-#pragma unroll
-      for (int t = 0; t < S::TW; t++) {
-        const u32x4 w = piece(wl + w_off(t));
-        const u32x4 f0 = f8_decode8(w[0], w[1]), f1 = f8_decode8(w[2], w[3]);
-#pragma unroll
-        for (int x = 0; x < S::TX; x++)
-          add(t, x, mfma16(f1, xf[x][1], mfma16(f0, xf[x][0], f32x4{0.f, 0.f, 0.f, 0.f})), sw[t / P]);
-      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    buf = buf + 1 == S::D ? 0 : buf + 1;
+    buf = next;
   }
+  add(S::TX - 1);
   wait_loads<0>();  // nothing writes LDS after the workgroup
 
   if constexpr (!SWIGLU) {
