@@ -101,6 +101,40 @@ def test_masks_and_non_finite_logits(dev, E, k, groups, top, scoring, with_bias,
     check(np.clip(l, -3e38, 3e38), k, dev, bias, torch.bfloat16, **kw)
 
 
+MANY = [dict(E=8, k=2), dict(E=16, k=15), dict(E=60, k=4), dict(E=64, k=8, groups=2, top_groups=1), dict(E=96, k=6, groups=3, top_groups=2),
+        dict(E=128, k=8), dict(E=128, k=8, groups=8, top_groups=3), dict(E=160, k=6, groups=8, top_groups=3), dict(E=250, k=13),
+        dict(E=256, k=8, groups=8, top_groups=4), dict(E=256, k=1, groups=16, top_groups=15), dict(E=256, k=15, groups=4, top_groups=4), dict(E=256, k=16)]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(str(v) for v in c.values()))
+def test_many_tokens(dev, case, scoring, with_bias, group_score):
+    """Enough tokens for four to a wave: spread and close logits, equal ones, masked and padded rows."""
+    print("many tokens", case, scoring, with_bias, group_score, flush=True)
+    case = dict(case)
+    E, k = case.pop("E"), case.pop("k")
+    rng = np.random.default_rng([14, E, k])
+    T = 4099
+    l = 2 * rng.standard_normal((T, E))
+    l[100:200] = 0.5 * rng.integers(-2, 3, (100, E))
+    l[200:300] = rng.standard_normal((100, 1)) + 1e-6 * rng.standard_normal((100, E))
+    l[300:500][rng.random((200, E)) < 0.6] = -np.inf
+    l[500:520], l[520:540] = 0.0, np.finfo(np.float32).min
+    l[540:600][rng.random((60, E)) < 0.2] = np.nan
+    l[600:620][rng.random((20, E)) < 0.1] = np.inf
+    l[4000:] = -np.inf
+    bias = 0.1 * rng.standard_normal(E) if with_bias else None
+    kw = dict(scoring=scoring, group_score=group_score, **case)
+    ids, w = check(l, k, dev, bias, **kw)
+    assert (ids[4000:] == -1).all() and not w[4000:].any()
+    check(l, k, dev, bias, renormalize=False, scale=2.5, **kw)
+    check(np.clip(l, -3e38, None), k, dev, bias, torch.bfloat16, **kw)
+    if with_bias:
+        check(l, k, dev, 0.5 * rng.integers(0, 2, E), torch.bfloat16, **kw)
+
+
 def test_close_scores(dev):
     """Scores with a bias that differ by less than fp32 can hold are told apart."""
     rng = np.random.default_rng(12)
