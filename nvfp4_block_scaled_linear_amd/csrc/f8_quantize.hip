@@ -52,25 +52,20 @@ __device__ __forceinline__ uint32_t largest_of_lanes(uint32_t m) {
   return m;
 }
 
-__device__ __forceinline__ u32x4 codes16(const float v[16], float s) {
-  u32x4 c;
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-    c[i] = f8_codes4(f8_ratio(v[4 * i], s), f8_ratio(v[4 * i + 1], s), f8_ratio(v[4 * i + 2], s), f8_ratio(v[4 * i + 3], s));
-  return c;
-}
-
-// ROWS = 1: thread by thread the blocks of rows in order, eight threads to a block
+// Threads of a workgroup: 2^shift side by side along a row, eight to a block, the rest down the
+// rows.
 template <int T, int RULE>
 __global__ __launch_bounds__(kThreads) void f8_quantize_rows(const void* x, int64_t ldx, int64_t M,
-                                                             int64_t K, int32_t kb, uint8_t* codes,
-                                                             float* scales, uint32_t* faults) {
-  const int64_t blocks = M * kb, lane = threadIdx.x % kLanes;
+                                                             int64_t K, int32_t kb, int shift,
+                                                             uint8_t* codes, float* scales,
+                                                             uint32_t* faults) {
+  const int64_t row = (int64_t)blockIdx.x * (kThreads >> shift) + (threadIdx.x >> shift);
+  if (row >= M) return;
+  const int pieces = kb * kLanes;  // of 16 values, of whole blocks
   bool bad = false;
   // whole groups of lanes leave together
-  for (int64_t b = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes; b < blocks;
-       b += (int64_t)gridDim.x * (kThreads / kLanes)) {
-    const int64_t row = b / kb, k = (b - row * kb) * kF8Block + 16 * lane;
+  for (int p = ((int)blockIdx.y << shift) + (threadIdx.x & ((1 << shift) - 1)); p < pieces; p += gridDim.y << shift) {
+    const int64_t k = 16 * (int64_t)p;
     const bool in = k < K;  // K % 16 == 0
     float v[16];
     if (in) {
@@ -83,8 +78,9 @@ __global__ __launch_bounds__(kThreads) void f8_quantize_rows(const void* x, int6
     const bool odd = amax >= 0x7F800000u;  // a NaN or Inf is the largest as bits
     bad = bad || odd;
     const float s = f8_scale<RULE>(__uint_as_float(amax));
-    if (in) *reinterpret_cast<u32x4*>(codes + row * K + k) = odd ? u32x4{0u, 0u, 0u, 0u} : codes16(v, s);
-    if (lane == 0) scales[b] = odd ? __uint_as_float(0x7FC00000u) : s;
+    if (in)
+      *reinterpret_cast<u32x4*>(codes + row * K + k) = odd ? u32x4{0u, 0u, 0u, 0u} : f8_codes16(v, __uint_as_float(amax), s);
+    if (p % kLanes == 0) scales[row * kb + p / kLanes] = odd ? __uint_as_float(0x7FC00000u) : s;
   }
   if (bad && faults) atomicOr(faults, (uint32_t)NVFP4_FAULT_NONFINITE);
 }
@@ -124,7 +120,7 @@ __global__ __launch_bounds__(kThreads) void f8_quantize_blocks(const void* x, in
 #pragma unroll
   for (int i = 0; i < kPer; i++)
     if (k < K && row0 + i * kRows < M)
-      *reinterpret_cast<u32x4*>(codes + (row0 + i * kRows) * K + k) = odd ? u32x4{0u, 0u, 0u, 0u} : codes16(v[i], s);
+      *reinterpret_cast<u32x4*>(codes + (row0 + i * kRows) * K + k) = odd ? u32x4{0u, 0u, 0u, 0u} : f8_codes16(v[i], __uint_as_float(amax), s);
   if (threadIdx.x == 0) {
     scales[b] = odd ? __uint_as_float(0x7FC00000u) : s;
     if (odd && faults) atomicOr(faults, (uint32_t)NVFP4_FAULT_NONFINITE);
@@ -134,10 +130,12 @@ __global__ __launch_bounds__(kThreads) void f8_quantize_blocks(const void* x, in
 template <int T>
 __global__ __launch_bounds__(kThreads) void f8_dequantize_rows(const uint8_t* codes, const float* scales,
                                                                int64_t M, int64_t K, int32_t kb,
-                                                               int row_shift, void* y, int64_t ldy) {
-  const int64_t pieces = K >> 4, all = M * pieces;
-  for (int64_t p = (int64_t)blockIdx.x * kThreads + threadIdx.x; p < all; p += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = p / pieces, k = (p - row * pieces) << 4;
+                                                               int row_shift, int shift, void* y, int64_t ldy) {
+  const int64_t row = (int64_t)blockIdx.x * (kThreads >> shift) + (threadIdx.x >> shift);
+  if (row >= M) return;
+  const int pieces = (int)(K >> 4);
+  for (int p = ((int)blockIdx.y << shift) + (threadIdx.x & ((1 << shift) - 1)); p < pieces; p += gridDim.y << shift) {
+    const int64_t k = 16 * (int64_t)p;
     const u32x4 c = *reinterpret_cast<const u32x4*>(codes + row * K + k);
     const float s = scales[(row >> row_shift) * kb + (k >> 7)];
     float v[16];
@@ -183,6 +181,20 @@ __global__ __launch_bounds__(kThreads) void f8_scan_codes(const uint8_t* p, int6
   if (hit) atomicOr(faults, (uint32_t)NVFP4_FAULT_NONFINITE);
 }
 
+// threads along a row of `pieces` (a power of two, at least 2^least) and the launch grid
+struct RowShape {
+  int shift;
+  dim3 grid;
+};
+
+RowShape row_shape(int64_t M, int64_t pieces, int least) {
+  int shift = least;
+  while (shift < 8 && ((int64_t)1 << shift) < pieces) shift++;
+  const int64_t gx = (M + (kThreads >> shift) - 1) / (kThreads >> shift);
+  const int64_t gy = (pieces + ((int64_t)1 << shift) - 1) >> shift;
+  return {shift, dim3((uint32_t)gx, (uint32_t)(gy < 1024 ? gy : 1024))};
+}
+
 // workgroups for n items of a thread each, at most `most`
 dim3 grid_of(int64_t n, int64_t most) {
   const int64_t g = (n + kThreads - 1) / kThreads;
@@ -195,30 +207,30 @@ hipError_t launch_f8_quantize(int x_type, const void* x, int64_t ldx, int64_t M,
                               int block_rows, int scale_rule, uint8_t* codes, float* scales,
                               uint32_t* faults, hipStream_t stream) {
   const int32_t kb = (int32_t)((K + kF8Block - 1) / kF8Block);
-  const auto launch = [&](auto k, dim3 grid) {
-    hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, stream, x, ldx, M, K, kb, codes, scales, faults);
-    return hipGetLastError();
-  };
   const bool bf16 = x_type == FP8_BF16, pow2 = scale_rule == FP8_SCALE_POW2;
   if (block_rows == 1) {
-    const dim3 grid = grid_of(M * kb * kLanes, 1 << 20);
-    return launch(bf16 ? pow2 ? f8_quantize_rows<FP8_BF16, FP8_SCALE_POW2> : f8_quantize_rows<FP8_BF16, FP8_SCALE_F32>
-                       : pow2 ? f8_quantize_rows<FP8_F32, FP8_SCALE_POW2> : f8_quantize_rows<FP8_F32, FP8_SCALE_F32>, grid);
+    const RowShape r = row_shape(M, kb * (int64_t)kLanes, 3);
+    auto k = bf16 ? pow2 ? f8_quantize_rows<FP8_BF16, FP8_SCALE_POW2> : f8_quantize_rows<FP8_BF16, FP8_SCALE_F32>
+                  : pow2 ? f8_quantize_rows<FP8_F32, FP8_SCALE_POW2> : f8_quantize_rows<FP8_F32, FP8_SCALE_F32>;
+    hipLaunchKernelGGL(k, r.grid, dim3(kThreads), 0, stream, x, ldx, M, K, kb, r.shift, codes, scales, faults);
+    return hipGetLastError();
   }
   const int64_t blocks = (M + kF8Block - 1) / kF8Block * kb;
   if (blocks * kThreads > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
-  return launch(bf16 ? pow2 ? f8_quantize_blocks<FP8_BF16, FP8_SCALE_POW2> : f8_quantize_blocks<FP8_BF16, FP8_SCALE_F32>
-                     : pow2 ? f8_quantize_blocks<FP8_F32, FP8_SCALE_POW2> : f8_quantize_blocks<FP8_F32, FP8_SCALE_F32>,
-                dim3((uint32_t)blocks));
+  auto k = bf16 ? pow2 ? f8_quantize_blocks<FP8_BF16, FP8_SCALE_POW2> : f8_quantize_blocks<FP8_BF16, FP8_SCALE_F32>
+                : pow2 ? f8_quantize_blocks<FP8_F32, FP8_SCALE_POW2> : f8_quantize_blocks<FP8_F32, FP8_SCALE_F32>;
+  hipLaunchKernelGGL(k, dim3((uint32_t)blocks), dim3(kThreads), 0, stream, x, ldx, M, K, kb, codes, scales, faults);
+  return hipGetLastError();
 }
 
 hipError_t launch_f8_dequantize(const uint8_t* codes, const float* scales, int64_t M, int64_t K,
                                 int block_rows, int y_type, void* y, int64_t ldy,
                                 hipStream_t stream) {
   const int32_t kb = (int32_t)((K + kF8Block - 1) / kF8Block);
+  const RowShape r = row_shape(M, K >> 4, 0);
   auto k = y_type == FP8_BF16 ? f8_dequantize_rows<FP8_BF16> : f8_dequantize_rows<FP8_F32>;
-  hipLaunchKernelGGL(k, grid_of(M * (K >> 4), 1 << 20), dim3(kThreads), 0, stream, codes, scales, M, K, kb,
-                     block_rows == 1 ? 0 : 7, y, ldy);
+  hipLaunchKernelGGL(k, r.grid, dim3(kThreads), 0, stream, codes, scales, M, K, kb, block_rows == 1 ? 0 : 7, r.shift,
+                     y, ldy);
   return hipGetLastError();
 }
 
