@@ -19,6 +19,7 @@ FP8_EXPORTS = ("fp8_quantize", "fp8_dequantize", "fp8_linear", "fp8_grouped_line
 _ACT_BF16, _ACT_FP8 = 0, 1
 _F8, _I32 = torch.float8_e4m3fn, torch.int32
 _X_TYPES, _X8_TYPES = (_BF16,), (_F8,)
+_strided = torch.empty_strided
 _BLOCK_ROWS = (1, 128)
 _SCORING = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORE = {"max": 0, "top2": 1}
@@ -52,11 +53,19 @@ def _codes(codes, scales, dims, index):
     shape = codes.shape
     if len(shape) != dims or codes.dtype is not _F8 or not codes.is_contiguous():
         raise ValueError(f"w_codes: contiguous {_F8} of {dims} dimensions is needed, got {codes.dtype} {tuple(shape)}")
-    return shape, codes.data_ptr(), _dense(scales, "w_scales", _F32, (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1])), index)
+    blocks = ((shape[-2] + 127) >> 7, (shape[-1] + 127) >> 7)
+    if dims == 3:
+        blocks = (shape[0], *blocks)
+    if scales.dtype is not _F32 or scales.shape != blocks or scales.get_device() != index or not scales.is_contiguous():
+        _dense(scales, "w_scales", _F32, blocks, index)  # says what is wrong
+    return shape, codes.data_ptr(), scales.data_ptr()
 
 
 def _acts(x, x_scales, K, index):
     """(kind, rows, x address, scales address, row pitch) of the activations."""
+    shape = x.shape
+    if x_scales is None and x.dtype is _BF16 and len(shape) == 2 and shape[1] == K and x.get_device() == index and x.is_contiguous():
+        return _ACT_BF16, shape[0], x.data_ptr(), None, K
     if x.get_device() != index:
         raise ValueError(f"x is on {x.device}, the weight on cuda:{index}")
     M, cols, ld = _rows(x, "x", _X_TYPES if x_scales is None else _X8_TYPES)
@@ -64,7 +73,7 @@ def _acts(x, x_scales, K, index):
         raise ValueError(f"x: rows of {K} values are needed, got {cols}")
     if x_scales is None:
         return _ACT_BF16, M, x.data_ptr(), None, ld
-    return _ACT_FP8, M, x.data_ptr(), _dense(x_scales, "x_scales", _F32, (M, _blocks(K)), index), ld
+    return _ACT_FP8, M, x.data_ptr(), _dense(x_scales, "x_scales", _F32, (M, (K + 127) >> 7), index), ld
 
 
 def _check_block_rows(block_rows):
@@ -79,18 +88,19 @@ def fp8_quantize(x, *, block_rows=1, pow2_scales=False, faults=None, codes=None,
     of two. `faults`: a device int32 that receives FAULT_NONFINITE."""
     index = _device(x)
     M, K, ld = _rows(x, "x", _TYPES)
-    _check_block_rows(block_rows)
+    if block_rows not in _BLOCK_ROWS:
+        _check_block_rows(block_rows)
+    down, along = M if block_rows == 1 else (M + 127) >> 7, (K + 127) >> 7
     if codes is None:
-        codes = _new((M, K), _F8, x)
+        codes = _strided((M, K), (K, 1), dtype=_F8, device=x.device)
         cp = codes.data_ptr()
     else:
         cp = _dense(codes, "codes", _F8, (M, K), index)
-    shape = (M if block_rows == 1 else _blocks(M), _blocks(K))
     if scales is None:
-        scales = _new(shape, _F32, x)
+        scales = _strided((down, along), (along, 1), dtype=_F32, device=x.device)
         sp = scales.data_ptr()
     else:
-        sp = _dense(scales, "scales", _F32, shape, index)
+        sp = _dense(scales, "scales", _F32, (down, along), index)
     _run((_lib or _load()).fp8_quantize, "fp8_quantize", index, _TYPES[x.dtype], x.data_ptr(), ld, M, K, block_rows,
          1 if pow2_scales else 0, cp, sp, None if faults is None else _word(faults, index))
     return codes, scales
@@ -121,9 +131,13 @@ def fp8_linear(x, w_codes, w_scales, *, x_scales=None, out=None, out_dtype=_F32,
     index = _device(w_codes)
     (N, K), cp, sp = _codes(w_codes, w_scales, 2, index)
     act, M, xp, xsp, ldx = _acts(x, x_scales, K, index)
-    out, ldy = _out(out, out_dtype, M, N, index, w_codes)
-    _run((_lib or _load()).fp8_linear, "fp8_linear", index, act, xp, xsp, ldx, M, N, K, cp, sp, _TYPES[out.dtype],
-         out.data_ptr(), ldy, F_CHECK if check else 0, None if faults is None else _word(faults, index))
+    if out is None and out_dtype in _TYPES:
+        out, y_type, ldy = _strided((M, N), (N, 1), dtype=out_dtype, device=w_codes.device), _TYPES[out_dtype], N
+    else:
+        out, ldy = _out(out, out_dtype, M, N, index, w_codes)
+        y_type = _TYPES[out.dtype]
+    _run((_lib or _load()).fp8_linear, "fp8_linear", index, act, xp, xsp, ldx, M, N, K, cp, sp, y_type, out.data_ptr(), ldy,
+         1 if check else 0, None if faults is None else _word(faults, index))
     return out
 
 
@@ -222,12 +236,12 @@ def moe_route(logits, top_k, *, scoring="softmax", bias=None, groups=1, top_grou
     bp = None if bias is None else _dense(bias, "bias", _F32, (E,), index)
     shape = (T, top_k)
     if topk_ids is None:
-        topk_ids = _new(shape, _I32, logits)
+        topk_ids = _strided(shape, (top_k, 1), dtype=_I32, device=logits.device)
         ip = topk_ids.data_ptr()
     else:
         ip = _dense(topk_ids, "topk_ids", _I32, shape, index)
     if topk_w is None:
-        topk_w = _new(shape, _F32, logits)
+        topk_w = _strided(shape, (top_k, 1), dtype=_F32, device=logits.device)
         wp = topk_w.data_ptr()
     else:
         wp = _dense(topk_w, "topk_w", _F32, shape, index)
