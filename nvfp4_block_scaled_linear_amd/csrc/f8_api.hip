@@ -175,8 +175,9 @@ nvfp4_status fp8_grouped_linear(int32_t act_kind, const void* x, const float* x_
   if (swiglu && N % (2 * kF8Block) != 0) return NVFP4_ERR_SHAPE;
   if (!fits(N, K)) return NVFP4_ERR_SHAPE;
   // rows that a later kernel of the call reads: fp32 to combine, BF16 to quantize
-  const size_t row_bytes = combine ? 4 * (size_t)N : to_f8 ? (size_t)N : 0;
   const RoutePlan plan = plan_routes(T, top_k, num_experts, kTiledRoutes, kTile128Routes);
+  const bool streams = plan.scan || plan.slots;  // (tiles quantize their own results)
+  const size_t row_bytes = combine ? 4 * (size_t)N : to_f8 && streams ? (size_t)N : 0;
   const RouteLayout L = layout_routes(plan, T, top_k, num_experts, row_bytes);
   if (!workspace) {
     *workspace_bytes = L.total;
@@ -206,17 +207,17 @@ nvfp4_status fp8_grouped_linear(int32_t act_kind, const void* x, const float* x_
   a.N = N; a.K = K;
   a.R = R; a.x_rows = xrows; a.rows_per_token = rows_mode == NVFP4_ROWS_PER_TOKEN ? 1 : 0;
   a.top_k = top_k; a.num_experts = num_experts;
-  a.y = combine || to_f8 ? rows : y; a.ldy = N; a.y_type = combine ? FP8_F32 : y_type;
-  a.swiglu = swiglu ? FP8_OUT_SWIGLU_BF16 : 0;
+  a.y = row_bytes ? rows : y; a.y_scales = y_scales; a.ldy = N; a.y_type = combine ? FP8_F32 : y_type;
+  a.swiglu = to_f8 && streams ? FP8_OUT_SWIGLU_BF16 : swiglu ? out_mode : 0;
   a.zero_dropped = !combine;
   hipError_t e = prepare_routes(a, plan, L, workspace, topk_ids, T, reuse, faults, s);
   const int kind = kernel_kind(act_kind, y_type);
   if (e == hipSuccess)
-    e = plan.scan || plan.slots ? launch_f8_stream(a, kind, (R + active - 1) / active, s) : launch_f8_tiled(a, kind, s);
+    e = streams ? launch_f8_stream(a, kind, (R + active - 1) / active, s) : launch_f8_tiled(a, kind, s);
   if (e != hipSuccess) return NVFP4_ERR_LAUNCH;
   if (combine)
     e = launch_mx_combine(static_cast<float*>(rows), N, topk_ids, topk_w, T, top_k, num_experts, N, y_type, y, N, s);
-  if (to_f8)
+  if (to_f8 && streams)
     e = launch_f8_quantize(FP8_BF16, rows, N / 2, R, N / 2, 1, FP8_SCALE_F32, static_cast<uint8_t*>(y),
                            y_scales, nullptr, s);
   return launch_status(e);

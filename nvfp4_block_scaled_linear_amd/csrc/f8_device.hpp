@@ -65,18 +65,19 @@ __device__ __forceinline__ float f8_ratio(float x, float s) {
   return __builtin_fminf(__builtin_fmaxf(q, -kF8Top), kF8Top);
 }
 
-// Codes of 16 values of a block whose largest magnitude is amax and scale s. The correctly rounded
+// Codes of n values of a block whose largest magnitude is amax and scale s. The correctly rounded
 // quotients by one reciprocal: with r the rounded 1 / s, x * r is within 1.5 ulp of x / s, one
 // correction by the remainder makes it a neighbour of x / s, and by Markstein's theorem the next
 // rounds correctly (five operations a value, a division takes a dozen). Remainders stay
 // representable wherever the quotient is more than half of E4M3's least, as long as s is not tiny.
 // Such quotients are at most 448 rounded up, which the encoder rounds to 448.
-__device__ __forceinline__ u32x4 f8_codes16(const float v[16], float amax, float s) {
-  float q[16];
+template <int n>
+__device__ __forceinline__ void f8_codes(const float* v, float amax, float s, uint32_t* codes) {
+  float q[n];
   if (amax >= 0x1p-70f) {
     const float r = 1.0f / s;
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
+    for (int i = 0; i < n; i++) {
       float c = v[i] * r;
       c = __builtin_fmaf(__builtin_fmaf(-c, s, v[i]), r, c);
       c = __builtin_fmaf(__builtin_fmaf(-c, s, v[i]), r, c);
@@ -84,12 +85,20 @@ __device__ __forceinline__ u32x4 f8_codes16(const float v[16], float amax, float
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; i++) q[i] = f8_ratio(v[i], s);
+    for (int i = 0; i < n; i++) q[i] = f8_ratio(v[i], s);
   }
-  u32x4 c;
 #pragma unroll
-  for (int i = 0; i < 4; i++) c[i] = f8_codes4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
-  return c;
+  for (int i = 0; i < n / 4; i++) codes[i] = f8_codes4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+}
+
+// n BF16 pairs as values
+template <int n>
+__device__ __forceinline__ void f8_values(const uint32_t* pairs, float* v) {
+#pragma unroll
+  for (int i = 0; i < n; i++) {
+    v[2 * i] = __uint_as_float(pairs[i] << 16);
+    v[2 * i + 1] = __uint_as_float(pairs[i] & 0xFFFF0000u);
+  }
 }
 
 }  // namespace nvfp4

@@ -52,6 +52,13 @@ __device__ __forceinline__ uint32_t largest_of_lanes(uint32_t m) {
   return m;
 }
 
+// 16 codes of a block with largest magnitude amax (bits) and scale s; of one that is not finite, 0
+__device__ __forceinline__ void store_codes(uint8_t* to, const float v[16], uint32_t amax, float s) {
+  u32x4 c = {0u, 0u, 0u, 0u};
+  if (amax < 0x7F800000u) f8_codes<16>(v, __uint_as_float(amax), s, reinterpret_cast<uint32_t*>(&c));
+  *reinterpret_cast<u32x4*>(to) = c;
+}
+
 // Threads of a workgroup: 2^shift side by side along a row, eight to a block, the rest down the
 // rows.
 template <int T, int RULE>
@@ -78,8 +85,7 @@ __global__ __launch_bounds__(kThreads) void f8_quantize_rows(const void* x, int6
     const bool odd = amax >= 0x7F800000u;  // a NaN or Inf is the largest as bits
     bad = bad || odd;
     const float s = f8_scale<RULE>(__uint_as_float(amax));
-    if (in)
-      *reinterpret_cast<u32x4*>(codes + row * K + k) = odd ? u32x4{0u, 0u, 0u, 0u} : f8_codes16(v, __uint_as_float(amax), s);
+    if (in) store_codes(codes + row * K + k, v, amax, s);
     if (p % kLanes == 0) scales[row * kb + p / kLanes] = odd ? __uint_as_float(0x7FC00000u) : s;
   }
   if (bad && faults) atomicOr(faults, (uint32_t)NVFP4_FAULT_NONFINITE);
@@ -120,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void f8_quantize_blocks(const void* x, in
 #pragma unroll
   for (int i = 0; i < kPer; i++)
     if (k < K && row0 + i * kRows < M)
-      *reinterpret_cast<u32x4*>(codes + (row0 + i * kRows) * K + k) = odd ? u32x4{0u, 0u, 0u, 0u} : f8_codes16(v[i], __uint_as_float(amax), s);
+      store_codes(codes + (row0 + i * kRows) * K + k, v[i], amax, s);
   if (threadIdx.x == 0) {
     scales[b] = odd ? __uint_as_float(0x7FC00000u) : s;
     if (odd && faults) atomicOr(faults, (uint32_t)NVFP4_FAULT_NONFINITE);

@@ -63,6 +63,28 @@ __device__ __forceinline__ int quarter_swizzle(int row) {
   return ((a & 1) << 1) ^ ((a >> 1) * 3);
 }
 
+// Eight values (BF16 ones) of a block, quantized. most: where the WW waves' largest magnitudes of the
+// row lie, `pitch` apart; *scale is the block's.
+template <int WW>
+__device__ __forceinline__ uint2 quantize_block8(const float* most, int pitch, const uint32_t (&pairs)[4], float* scale) {
+  float amax = most[0];
+#pragma unroll
+  for (int w = 1; w < WW; w++) {  // (as bits: what is not finite is largest)
+    const float m = most[w * pitch];
+    amax = __float_as_uint(m) > __float_as_uint(amax) ? m : amax;
+  }
+  if (__float_as_uint(amax) >= 0x7F800000u) {
+    *scale = __uint_as_float(0x7FC00000u);
+    return make_uint2(0u, 0u);
+  }
+  *scale = f8_scale<FP8_SCALE_F32>(amax);
+  float v[8];
+  uint32_t codes[2];
+  f8_values<4>(pairs, v);
+  f8_codes<8>(v, amax, *scale, codes);
+  return make_uint2(codes[0], codes[1]);
+}
+
 template <class S, bool GROUPED, int SWIGLU>
 __global__ __launch_bounds__(S::T) __attribute__((amdgpu_waves_per_eu(S::T == 512 ? 2 : 1, 2)))
 void f8_tiled(F8Args a, int gm, int vec) {
@@ -79,6 +101,14 @@ void f8_tiled(F8Args a, int gm, int vec) {
   constexpr int BC = SWIGLU ? S::BN / 2 : S::BN;  // output columns of a tile
   const uint32_t nbn = (uint32_t)((cols + BC - 1) / BC);
 
+  // What every workgroup does in the end: its share of dropped routes' rows, if the grouping has
+  // fewer places than there are routes (looking for them took 6 of 200 us where there are none).
+  const bool dropped = GROUPED && a.offsets[a.num_experts] < (int32_t)a.R;
+  const auto finish = [&] {
+    if constexpr (GROUPED) {
+      if (dropped) clear_dropped<SWIGLU>(a);
+    }
+  };
   // tile of this workgroup: each XCD (blockIdx % 8) takes a run of tiles, which share
   // operands through its L2 (the parts of a list tile among them)
   int64_t mt, nt;
@@ -88,10 +118,12 @@ void f8_tiled(F8Args a, int gm, int vec) {
     uint32_t nbm = GROUPED ? *a.n_tiles : (uint32_t)((a.M + S::BM - 1) / S::BM);
     if (GROUPED) {
       nbm = nbm < (uint32_t)a.max_tiles ? nbm : (uint32_t)a.max_tiles;
-      clear_dropped<SWIGLU>(a);
     }
     const uint32_t total = nbm * nbn * parts;
-    if (blockIdx.x >= total) return;
+    if (blockIdx.x >= total) {
+      finish();
+      return;
+    }
     const uint32_t q = total / 8, r = total % 8, x = blockIdx.x % 8;
     uint32_t lin = x * q + (x < r ? x : r) + blockIdx.x / 8;
     if (GROUPED) {
@@ -107,12 +139,19 @@ void f8_tiled(F8Args a, int gm, int vec) {
   const uint8_t* wc = a.w_codes;
   const float* ws = a.w_scales;
   int64_t m0 = 0, rows_m;
-  int32_t slot0 = 0;
+  int32_t slot0 = 0, route[GROUPED ? S::NX : 1], scale_route = 0;
   if (GROUPED) {
     const int e = in_experts(a, a.tiles[2 * mt]);
     slot0 = in_routes(a, a.tiles[2 * mt + 1]) + part * S::BM;
+    // the routes of this lane's loads, not waiting for how many there are
+#pragma unroll
+    for (int i = 0; i < S::NX; i++) route[i] = a.sorted[in_routes(a, slot0 + i * S::RX + (tid >> 3))];
+    scale_route = S::F8 ? a.sorted[in_routes(a, slot0 + tid)] : 0;
     rows_m = run_length(a, slot0, a.offsets[e + 1], S::BM);
-    if (rows_m == 0) return;
+    if (rows_m == 0) {
+      finish();
+      return;
+    }
     wc += (int64_t)e * N * K;
     ws += (int64_t)e * ((N + 127) >> 7) * kb;
   } else {
@@ -120,11 +159,9 @@ void f8_tiled(F8Args a, int gm, int vec) {
     rows_m = a.M - m0 < S::BM ? a.M - m0 : S::BM;
   }
 
-  // x row of tile row r (grouped: relative to x, dense: to the tile's first row)
-  const auto x_row = [&](int r) -> int64_t {
-    if (!GROUPED) return r;
-    const int32_t route = a.sorted[slot0 + r];
-    return a.rows_per_token ? route / a.top_k : route;
+  // x row of a route
+  const auto x_row = [&](int32_t route) -> int64_t {
+    return a.rows_per_token ? (uint32_t)route / (uint32_t)a.top_k : (uint32_t)route;
   };
   constexpr int XE = S::F8 ? 1 : 2;  // bytes of an activation
   const int64_t xpitch = a.ldx * XE;
@@ -150,8 +187,10 @@ void f8_tiled(F8Args a, int gm, int vec) {
     xk = q * (16 / XE);
 #pragma unroll
     for (int i = 0; i < (GROUPED ? S::NX : 1); i++) {
-      const int ri = i * S::RX + r;
-      xo[i] = ri < rows_m || !GROUPED ? (uint32_t)(x_row(ri) * xpitch) + 16 * q : kOutOfRange;
+      if constexpr (GROUPED)
+        xo[i] = i * S::RX + r < rows_m ? (uint32_t)(x_row(route[i]) * xpitch) + 16 * q : kOutOfRange;
+      else
+        xo[i] = (uint32_t)(r * xpitch) + 16 * q;
     }
   }
   {
@@ -177,7 +216,7 @@ void f8_tiled(F8Args a, int gm, int vec) {
   uint32_t so = kOutOfRange;
   if (S::F8) {
     xsr = lds_load_rsrc(a.x_scales + (GROUPED ? 0 : m0 * kb), 4 * x_last * kb);
-    if (tid < S::BM && tid < rows_m) so = (uint32_t)(4 * x_row(tid) * kb);
+    if (tid < S::BM && tid < rows_m) so = (uint32_t)(4 * (GROUPED ? x_row(scale_route) : tid) * kb);
   }
 
   const uint32_t lds0 = lds_address(smem);
@@ -200,6 +239,27 @@ void f8_tiled(F8Args a, int gm, int vec) {
     }
   };
 
+  // scales of this wave's groups of weight rows
+  const float* wsp[GROUPS];
+#pragma unroll
+  for (int i = 0; i < GROUPS; i++) {
+    const int64_t n = SWIGLU ? n0 + ww * 32 + i * half : n0 + ww * 64;
+    wsp[i] = ws + (n < N ? n >> 7 : 0) * kb;
+  }
+  // this lane's scale of each group, of 64 blocks from b on; waited for by themselves, because a wait
+  // at their use would be for loads into LDS as well
+  float w_scale[GROUPS];
+  const auto load_scales = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < GROUPS; i++) w_scale[i] = b + lane < kb ? wsp[i][b + lane] : 0.f;
+  };
+  const auto wait_scales = [&] {
+#pragma unroll
+    for (int i = 0; i < GROUPS; i++) asm volatile("" : "+v"(w_scale[i]));
+  };
+  load_scales(0);
+  const int steps = (K + S::SK - 1) / S::SK;
+  const auto piece = [](const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); };
   f32x4 acc[S::TW][S::TX];
 #pragma unroll
   for (int t = 0; t < S::TW; t++)
@@ -210,13 +270,6 @@ void f8_tiled(F8Args a, int gm, int vec) {
   // 4a + b
   const auto w_group = [&](int t) { return SWIGLU ? t / P * BC + ww * 16 * P : (ww * GROUPS + t / P) * 16 * P; };
   const auto w_local = [&](int t, int row) { return w_group(t) + 4 * P * (row >> 2) + 4 * (t % P) + (row & 3); };
-  // scales of this wave's groups
-  const float* wsp[GROUPS];
-#pragma unroll
-  for (int i = 0; i < GROUPS; i++) {
-    const int64_t n = SWIGLU ? n0 + ww * 16 * P + i * half : n0 + w_group(i * P);
-    wsp[i] = ws + (n < N ? n >> 7 : 0) * kb;
-  }
   // where this lane reads: its pieces of an activation row and of a weight row (the second lies 64
   // bytes on or back), and the row's scale
   const int xrow = wx * S::TX * 16 + c;
@@ -230,7 +283,6 @@ void f8_tiled(F8Args a, int gm, int vec) {
   };
   static_assert(SWIGLU || GROUPS == 1, "");
 
-  const auto piece = [](const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); };
   u32x4 wf[S::TW][S::KF], xq[2][2];
   float sx[2];
   const auto read_w = [&](int buf) {
@@ -273,24 +325,18 @@ void f8_tiled(F8Args a, int gm, int vec) {
 #pragma unroll
   for (int i = 0; i < GROUPS; i++) sc[1][i] = 0.f;
 
-  // this lane's scale of each group, of 64 blocks from b on; waited for by themselves, because a wait
-  // at their use would be for loads into LDS as well
-  float w_scale[GROUPS];
-  const auto load_scales = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < GROUPS; i++) w_scale[i] = b + lane < kb ? wsp[i][b + lane] : 0.f;
-  };
-  const auto wait_scales = [&] {
-#pragma unroll
-    for (int i = 0; i < GROUPS; i++) asm volatile("" : "+v"(w_scale[i]));
-  };
-  load_scales(0);
-  const int steps = (K + S::SK - 1) / S::SK;
+  // (a group's weight first: its activations' rows are still being looked up)
 #pragma unroll
   for (int s = 0; s < S::D - 1; s++)
 #pragma unroll
-    for (int i = 0; i < S::LOADS; i++) issue(s, s, i);
-  wait_loads_barrier<(S::D - 2) * S::LOADS>();
+    for (int i = S::NX; i < S::NX + S::NW; i++) issue(s, s, i);
+#pragma unroll
+  for (int s = 0; s < S::D - 1; s++) {
+#pragma unroll
+    for (int i = 0; i < S::NX; i++) issue(s, s, i);
+    if (S::NS) issue(s, s, S::NX + S::NW);
+  }
+  wait_loads_barrier<(S::D - 2) * (S::NX + S::NS)>();
   read_w(0);
   read_x(0, 0, 0);
   wait_scales();
@@ -353,44 +399,84 @@ void f8_tiled(F8Args a, int gm, int vec) {
     buf = next;
   }
   add(S::TX - 1);
-  wait_loads<0>();  // nothing writes LDS after the workgroup
+  wait_loads_barrier<0>();  // nothing writes LDS after this, and the other waves have read their last stage
 
-  if constexpr (!SWIGLU) {
-    wait_loads_barrier<0>();  // the other waves have read their last stage
+  if constexpr (SWIGLU == 0) {
     const int64_t n = n0 + ww * S::TW * 16;
     uint8_t* const out = smem + wave * store_bytes<S>();
-    if (n >= N) return;
-    if (a.y_type == FP8_F32)
-      store_tile<S, GROUPED, 4>(a, out, acc, wx, m0, slot0, rows_m, n, N - n, vec);
-    else
-      store_tile<S, GROUPED, 2>(a, out, acc, wx, m0, slot0, rows_m, n, N - n, vec);
-    return;
-  }
-#pragma unroll
-  for (int x = 0; x < S::TX; x++) {
-    const int r = (wx * S::TX + x) * 16 + c;
-    if (r >= rows_m) continue;
-    const int64_t row = GROUPED ? route_at(a, slot0 + r) : m0 + r;
-    // SwiGLU: tile t and tile P + t are gate and up of the same columns
-    const int64_t n = n0 + w_local(0, 4 * g);
-    uint32_t h[2 * P];  // BF16 pairs of 4P consecutive columns
-#pragma unroll
-    for (int s = 0; s < P; s++) {
-      const f32x4 gt = acc[s][x], u = acc[P + s][x];
-      h[2 * s] = bf16_pair(silu(gt[0]) * u[0], silu(gt[1]) * u[1]);
-      h[2 * s + 1] = bf16_pair(silu(gt[2]) * u[2], silu(gt[3]) * u[3]);
+    if (n < N) {
+      if (a.y_type == FP8_F32)
+        store_tile<S, GROUPED, 4>(a, out, acc, wx, m0, slot0, rows_m, n, N - n, vec);
+      else
+        store_tile<S, GROUPED, 2>(a, out, acc, wx, m0, slot0, rows_m, n, N - n, vec);
     }
-    uint16_t* d = static_cast<uint16_t*>(a.y) + row * half + n;
-    if (vec && n + 4 * P <= half) {
+  } else {
+    // tile t and tile P + t are gate and up of the same columns
+    const int64_t n = n0 + w_local(0, 4 * g);
+    uint32_t pair[S::TX][2 * P];  // BF16 pairs of 4P consecutive columns
 #pragma unroll
-      for (int s = 0; s < P / 2; s++)
-        reinterpret_cast<u32x4*>(d)[s] = u32x4{h[4 * s], h[4 * s + 1], h[4 * s + 2], h[4 * s + 3]};
+    for (int x = 0; x < S::TX; x++)
+#pragma unroll
+      for (int s = 0; s < P; s++) {
+        const f32x4 gt = acc[s][x], u = acc[P + s][x];
+        pair[x][2 * s] = bf16_pair(silu(gt[0]) * u[0], silu(gt[1]) * u[1]);
+        pair[x][2 * s + 1] = bf16_pair(silu(gt[2]) * u[2], silu(gt[3]) * u[3]);
+      }
+    if constexpr (SWIGLU == FP8_OUT_SWIGLU_FP8) {
+      // The tile's columns are a block: the waves exchange each row's largest magnitudes, and the codes
+      // go out through LDS, a row's 128 bytes side by side.
+      static_assert(BC == 128 && P == 2, "");
+      float* const most = reinterpret_cast<float*>(smem);  // [WW][BM]
+      float* const scales = most + S::WW * S::BM;          // [BM]
+      uint8_t* const out = smem + 4 * (S::WW + 1) * S::BM;  // [BM][128], pieces of 16 as in the operands
+      static_assert((4 * (S::WW + 1) + 128) * S::BM <= S::LDS, "");
+#pragma unroll
+      for (int x = 0; x < S::TX; x++) {
+        uint32_t m = amax_pairs<4>(pair[x]);
+        uint32_t o = __shfl_xor(m, 16, 64);
+        m = m > o ? m : o;
+        o = __shfl_xor(m, 32, 64);
+        m = m > o ? m : o;
+        if (g == 0) most[ww * S::BM + xrow + 16 * x] = __uint_as_float(m);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < S::TX; x++) {
+        const int r = xrow + 16 * x;
+        float scale;
+        const uint2 codes = quantize_block8<S::WW>(most + r, S::BM, pair[x], &scale);
+        *reinterpret_cast<uint2*>(out + r * 128 + (((2 * ww + (g >> 1)) ^ ((r >> 1) & 7)) << 4) + 8 * (g & 1)) = codes;
+        if (ww == 0 && g == 0) scales[r] = scale;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < S::BM / (S::T / 8); i++) {
+        const int r = i * (S::T / 8) + (tid >> 3), q = tid & 7;
+        if (r >= rows_m) break;
+        const int64_t row = GROUPED ? route_at(a, slot0 + r) : m0 + r;
+        *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.y) + row * half + n0 + 16 * q) =
+            *reinterpret_cast<const u32x4*>(out + r * 128 + ((q ^ ((r >> 1) & 7)) << 4));
+        if (q == 0) a.y_scales[row * (half >> 7) + (n0 >> 7)] = scales[r];
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4 * P; i++)
-        if (n + i < half) d[i] = (uint16_t)(h[i >> 1] >> (16 * (i & 1)));
+      for (int x = 0; x < S::TX; x++) {
+        const int r = xrow + 16 * x;
+        if (r >= rows_m) continue;
+        const int64_t row = GROUPED ? route_at(a, slot0 + r) : m0 + r;
+        uint16_t* const d = static_cast<uint16_t*>(a.y) + row * half + n;
+        if (vec) {
+#pragma unroll
+          for (int s = 0; s < P / 2; s++)
+            reinterpret_cast<u32x4*>(d)[s] = u32x4{pair[x][4 * s], pair[x][4 * s + 1], pair[x][4 * s + 2], pair[x][4 * s + 3]};
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4 * P; i++) d[i] = (uint16_t)(pair[x][i >> 1] >> (16 * (i & 1)));
+        }
+      }
     }
   }
+  finish();
 }
 
 // most rows of a tile of a grouped product
@@ -410,7 +496,15 @@ hipError_t launch_shape(const F8Args& a, hipStream_t stream) {
   const int vec = ((uintptr_t)a.y | (uintptr_t)(ld * ysz)) % 16 == 0;
   auto k = f8_tiled<S, false, 0>;
   if constexpr (S::BM <= grouped_rows(S::ACT)) {
-    if (a.tiles) k = a.swiglu ? f8_tiled<S, true, FP8_OUT_SWIGLU_BF16> : f8_tiled<S, true, 0>;
+    if (a.tiles) {
+      k = f8_tiled<S, true, 0>;
+      if constexpr (S::ACT != kF8Exact) {  // SwiGLU's results are not fp32
+        if (a.swiglu == FP8_OUT_SWIGLU_BF16) k = f8_tiled<S, true, FP8_OUT_SWIGLU_BF16>;
+        if constexpr (S::BN == 256) {
+          if (a.swiglu == FP8_OUT_SWIGLU_FP8) k = f8_tiled<S, true, FP8_OUT_SWIGLU_FP8>;
+        }
+      }
+    }
   }
   hipLaunchKernelGGL(k, dim3((uint32_t)groups), dim3(S::T), S::LDS, stream, a, gm, vec);
   return hipGetLastError();
@@ -434,9 +528,10 @@ hipError_t launch_act(const F8Args& a, hipStream_t stream) {
   if constexpr (ACT != kF8Exact) {  // (whose decoded operands leave no registers for it)
     if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_shape<Shape<ACT, 256, 256, 2, 4, F8 ? 2 : 3>>(a, stream);
   }
-  if (rows > 64 && tiles(128, 256) >= kFewTiles) return launch_shape<Shape<ACT, 128, 256, 2, 4, 3>>(a, stream);
+  const bool block = a.swiglu == FP8_OUT_SWIGLU_FP8;  // a tile's columns have to be one
+  if (rows > 64 && (block || tiles(128, 256) >= kFewTiles)) return launch_shape<Shape<ACT, 128, 256, 2, 4, 3>>(a, stream);
   if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_shape<Shape<ACT, 128, 128, 2, 2, F8 ? 3 : 4>>(a, stream);
-  if (tiles(64, 256) >= kFewTiles) return launch_shape<Shape<ACT, 64, 256, F8 ? 2 : 1, 4, 3>>(a, stream);
+  if (block || tiles(64, 256) >= kFewTiles) return launch_shape<Shape<ACT, 64, 256, F8 ? 2 : 1, 4, 3>>(a, stream);
   return launch_shape<Shape<ACT, 64, 128, 2, 2, F8 ? 3 : 4>>(a, stream);
 }
 

@@ -2,6 +2,7 @@
 // (MxArgs, F8Args), whose members of the grouped form have the same names.
 #pragma once
 
+#include "fp8.h"
 #include "mx_device.hpp"
 #include "mx_kernels.hpp"
 
@@ -50,14 +51,15 @@ template <int SWIGLU, class A>
 __device__ __forceinline__ void clear_route(const A& a, int64_t r) {
   const int lane = threadIdx.x & 63;
   const int64_t bytes = SWIGLU == 0 ? a.N * (a.y_type == MXFP4_F32 ? 4 : 2)
-                        : SWIGLU == MXFP4_OUT_SWIGLU_BF16 ? a.N : a.N >> 2;
+                        : SWIGLU == MXFP4_OUT_SWIGLU_BF16 ? a.N : SWIGLU == MXFP4_OUT_SWIGLU_MXFP4 ? a.N >> 2 : a.N >> 1;
   uint8_t* const row = static_cast<uint8_t*>(a.y) + r * bytes;
   if ((((uintptr_t)a.y | (uintptr_t)bytes) & 3) == 0)
     for (int64_t b = 4 * lane; b < bytes; b += 256) *reinterpret_cast<uint32_t*>(row + b) = 0u;
   else
     for (int64_t b = 2 * lane; b < bytes; b += 128) *reinterpret_cast<uint16_t*>(row + b) = 0;
-  if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4)
-    for (int64_t b = lane; b < a.N >> 6; b += 64) a.y_scales[r * (a.N >> 6) + b] = 0;
+  constexpr int shift = SWIGLU == MXFP4_OUT_SWIGLU_MXFP4 ? 6 : 8;  // columns of a block, gate and up
+  if (SWIGLU == MXFP4_OUT_SWIGLU_MXFP4 || SWIGLU == FP8_OUT_SWIGLU_FP8)
+    for (int64_t b = lane; b < a.N >> shift; b += 64) a.y_scales[r * (a.N >> shift) + b] = 0;
 }
 
 // The output rows of dropped routes become zeros, each by one wave, shared out over the launch:
