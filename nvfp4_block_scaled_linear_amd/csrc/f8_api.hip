@@ -78,15 +78,26 @@ int kernel_kind(int32_t act_kind, int32_t y_type) {
 
 int64_t x_pitch(int32_t act_kind, int64_t ldx) { return act_kind == FP8_ACT_FP8 ? ldx : ldx * 2; }
 
-// Whether a dense product streams the weight or takes LDS tiles.
+// Whether a dense product streams the weight, for runs of 48 (BF16 activations) or 64 rows x 32
+// columns, or takes LDS tiles. Up to 32 rows the weight is read once. For more, what counts is how
+// many such runs there are for 256 CUs: K = 4096, BF16, 384 of them (128 x 4096) take 19.7 us against
+// 32.4 in tiles, 768 (256 x 4096) 28.9 against 33.1, 1152 (128 x 12288) 47.0 against 33.6; W8A8, 256
+// take 9.0 against 18.7, 512 16.4 against 18.9, 768 25.4 against 19.5; with fp32 results 512 19.9
+// against 26.9, 768 28.8 against 27.6. Both sides grow with K, tiles less while launches of few
+// stages cost their latency: with K = 512 704 runs take 10.7 against 7.4 (BF16), with 1024 448 take
+// 9.0 against 7.7 (W8A8).
 bool streams(int32_t kind, int64_t M, int64_t N) {
-  return M <= 32 || (M + 63) / 64 * ((N + 31) / 32) <= 300;
+  const int64_t rows = kind == FP8_ACT_BF16 ? 48 : 64, most = kind == FP8_ACT_BF16 ? 600 : kind == FP8_ACT_FP8 ? 550 : 700;
+  return M <= 32 || (M + rows - 1) / rows * ((N + 31) / 32) <= most;
 }
 
 // Routes per active expert from which the grouped call works in tiles, and in tiles of 128
-// routes (see RoutePlan).
-constexpr int64_t kTiledRoutes = 16;
-constexpr int64_t kTile128Routes = 64;
+// routes (see RoutePlan). 32 experts, top-4, 2048 / 1024: gate_up and down of 64 tokens take 35 + 23
+// us by slots and 30 + 25 in tiles (W8A8 37 + 20 and 29 + 23), of 96 tokens 42 + 28 and 30 + 26 (43 +
+// 25 and 30 + 24). 512 tokens take 44 + 37 in tiles of 64 and 59 + 45 in tiles of 128 (44 + 36 and 52
+// + 40), 1024 tokens 65 + 52 and 66 + 53 (62 + 51 and 56 + 46).
+constexpr int64_t kTiledRoutes = 8;
+constexpr int64_t kTile128Routes = 96;
 
 }  // namespace
 

@@ -510,28 +510,55 @@ hipError_t launch_shape(const F8Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The largest tile that still makes about a workgroup per CU is taken: larger ones read the
+// Dense products take the tile that is done first: workgroups by the rounds that 256 CUs take them
+// in, times what a stage of 128 k costs in such a tile (in 10 ns, K = 4096, rounds that are full or
+// nearly so: W8A8 512 x 4096 in 256 tiles of 64 x 128 takes 19.8 us, 1024 x 4096 in 256 of 128 x 128
+// 25.6, 1024 x 8192 in 256 of 128 x 256 38.2, 4096 x 4096 in 256 of 256 x 256 61). Two of the smallest
+// fit a CU, and are done together sooner than one after the other (1024 tiles take 49 us). 1500 x
+// 6000 x 2048 takes 33 us in 144 tiles of 256 x 256, 39 in 288 of 128 x 256. The fp32 results of W8A8
+// decode both operands, which leaves no registers for the largest tile.
+struct TileCost {
+  int bm, bn;
+  int alone[3], pair[3];  // by kind of activations; 0: no such tile, no two on a CU
+};
+constexpr TileCost kTileCosts[] = {{256, 256, {356, 191, 0}, {0, 0, 0}},   {128, 256, {205, 117, 190}, {0, 0, 0}},
+                                   {128, 128, {133, 80, 127}, {0, 0, 0}},  {64, 256, {134, 82, 118}, {0, 0, 0}},
+                                   {64, 128, {108, 62, 92}, {137, 77, 118}}};
+
+// Grouped ones take the largest tile that still makes about a workgroup per CU: larger ones read the
 // operands less often.
 constexpr int64_t kFewTiles = 200;
 
 template <int ACT>
 hipError_t launch_act(const F8Args& a, hipStream_t stream) {
   constexpr bool F8 = ACT != FP8_ACT_BF16;
-  const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
-  const int64_t active = a.R < a.num_experts ? a.R : a.num_experts;
-  // workgroups that tiles of bm rows and bn weight rows make (grouped: about)
-  const auto tiles = [&](int64_t bm, int64_t bn) {
-    const int64_t bc = a.swiglu ? bn / 2 : bn;
-    return (a.tiles ? a.R / bm + active : (a.M + bm - 1) / bm) * ((cols + bc - 1) / bc);
-  };
-  const int64_t rows = !a.tiles ? a.M : a.tile_rows < grouped_rows(ACT) ? a.tile_rows : grouped_rows(ACT);
-  if constexpr (ACT != kF8Exact) {  // (whose decoded operands leave no registers for it)
-    if (rows > 128 && tiles(256, 256) >= kFewTiles) return launch_shape<Shape<ACT, 256, 256, 2, 4, F8 ? 2 : 3>>(a, stream);
+  int bm = 64, bn = 128;
+  if (a.tiles) {
+    const int64_t cols = a.swiglu ? a.N >> 1 : a.N;
+    const int64_t active = a.R < a.num_experts ? a.R : a.num_experts;
+    // workgroups that tiles of m rows and n weight rows make, about
+    const auto tiles = [&](int64_t m, int64_t n) { return (a.R / m + active) * ((cols + n - 1) / n); };
+    const bool block = a.swiglu == FP8_OUT_SWIGLU_FP8;  // a tile's columns have to be one
+    if (a.tile_rows > 64 && grouped_rows(ACT) > 64) bm = 128;
+    if (block || tiles(bm, a.swiglu ? 128 : 256) >= kFewTiles) bn = 256;
+  } else {
+    int64_t best = INT64_MAX;
+    for (const TileCost& c : kTileCosts) {
+      const int64_t alone = c.alone[ACT], pair = c.pair[ACT];
+      const int64_t rounds = ((a.M + c.bm - 1) / c.bm * ((a.N + c.bn - 1) / c.bn) + 255) / 256;
+      const int64_t cost = pair ? rounds / 2 * pair + rounds % 2 * alone : rounds * alone;
+      if (alone == 0 || cost >= best) continue;
+      best = cost;
+      bm = c.bm;
+      bn = c.bn;
+    }
   }
-  const bool block = a.swiglu == FP8_OUT_SWIGLU_FP8;  // a tile's columns have to be one
-  if (rows > 64 && (block || tiles(128, 256) >= kFewTiles)) return launch_shape<Shape<ACT, 128, 256, 2, 4, 3>>(a, stream);
-  if (rows > 64 && (a.tiles || tiles(128, 128) >= kFewTiles)) return launch_shape<Shape<ACT, 128, 128, 2, 2, F8 ? 3 : 4>>(a, stream);
-  if (block || tiles(64, 256) >= kFewTiles) return launch_shape<Shape<ACT, 64, 256, F8 ? 2 : 1, 4, 3>>(a, stream);
+  if constexpr (ACT != kF8Exact) {
+    if (bm == 256) return launch_shape<Shape<ACT, 256, 256, 2, 4, F8 ? 2 : 3>>(a, stream);
+  }
+  if (bm == 128 && bn == 256) return launch_shape<Shape<ACT, 128, 256, 2, 4, 3>>(a, stream);
+  if (bm == 128) return launch_shape<Shape<ACT, 128, 128, 2, 2, F8 ? 3 : 4>>(a, stream);
+  if (bn == 256) return launch_shape<Shape<ACT, 64, 256, F8 ? 2 : 1, 4, 3>>(a, stream);
   return launch_shape<Shape<ACT, 64, 128, 2, 2, F8 ? 3 : 4>>(a, stream);
 }
 
