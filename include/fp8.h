@@ -108,7 +108,7 @@ nvfp4_status fp8_linear(int32_t act_kind, const void* x, const float* x_scales, 
  *            sum over t's routes in ascending expert id of topk_w[t][j] * (x_row(r) w_e^T),
  *            accumulated in fp32 in that order.
  * y_scales must be NULL in the other modes. topk_w is ignored unless combining. W8A8 sums as in
- * fp8_linear, by y_type.
+ * fp8_linear, by y_type; SwiGLU's are fp32 ones, because its results are quantized again.
  * Rows of dropped routes are zeros (FP8: codes 0 and scales 0).
  * The workspace of every out_mode begins with the grouping, so one that is large enough for
  * both serves a layer's gate_up and down calls.

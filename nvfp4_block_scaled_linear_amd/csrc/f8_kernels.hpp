@@ -13,7 +13,7 @@ namespace nvfp4 {
 constexpr int kF8Block = 128;  // k of a block of scales, and weight rows
 
 // Beside FP8_ACT_*: FP8 activations whose products are summed in fp32 throughout (see mfma_f8),
-// for results that are asked for in fp32
+// for fp32 results and SwiGLU's
 constexpr int kF8Exact = 2;
 
 // One product x W^T, dense or grouped by expert. The members of the grouped form are those of

@@ -332,7 +332,7 @@ __global__ __launch_bounds__(64 * C::W) void f8_stream(F8Args a) {
 }
 
 // Dense forms have no SwiGLU, and among the grouped ones those of four weight tiles have nothing
-// else.
+// else (and none of them is FAST).
 template <class C, int MODE>
 hipError_t launch_mode(const F8Args& a, int64_t groups, hipStream_t stream) {
   constexpr bool SWIGLU = MODE != kDense && C::NT == 4;
@@ -372,7 +372,9 @@ hipError_t launch_act(const F8Args& a, int64_t rows, hipStream_t stream) {
   // a BF16 form of four rows loads no activations for the 12 others of the MFMA
   if (a.ids || a.slots) {
     constexpr int FEW = F8 ? 16 : 4;
-    if (a.swiglu) return rows <= 2 ? launch_rows<ACT, FEW, 4, 4, 2, true>(a, stream) : launch_rows<ACT, 16, 4, 4, 2, true>(a, stream);
+    if constexpr (ACT != FP8_ACT_FP8) {
+      if (a.swiglu) return rows <= 2 ? launch_rows<ACT, FEW, 4, 4, 2, true>(a, stream) : launch_rows<ACT, 16, 4, 4, 2, true>(a, stream);
+    }
     return rows <= 2 ? launch_rows<ACT, FEW, 2, 2, 2, true>(a, stream) : launch_rows<ACT, 16, 2, 2, 2, true>(a, stream);
   }
   if (rows <= 4) return launch_dense<ACT, F8 ? 16 : 4, F8 ? 3 : 2>(a, stream);

@@ -480,7 +480,7 @@ void f8_tiled(F8Args a, int gm, int vec) {
 }
 
 // most rows of a tile of a grouped product
-constexpr int grouped_rows(int act) { return act == FP8_ACT_FP8 ? 128 : 64; }
+constexpr int grouped_rows(int act) { return act == FP8_ACT_BF16 ? 64 : 128; }
 
 template <class S>
 hipError_t launch_shape(const F8Args& a, hipStream_t stream) {
@@ -498,7 +498,7 @@ hipError_t launch_shape(const F8Args& a, hipStream_t stream) {
   if constexpr (S::BM <= grouped_rows(S::ACT)) {
     if (a.tiles) {
       k = f8_tiled<S, true, 0>;
-      if constexpr (S::ACT != kF8Exact) {  // SwiGLU's results are not fp32
+      if constexpr (!S::FAST) {  // (which SwiGLU's products are not)
         if (a.swiglu == FP8_OUT_SWIGLU_BF16) k = f8_tiled<S, true, FP8_OUT_SWIGLU_BF16>;
         if constexpr (S::BN == 256) {
           if (a.swiglu == FP8_OUT_SWIGLU_FP8) k = f8_tiled<S, true, FP8_OUT_SWIGLU_FP8>;
