@@ -251,7 +251,7 @@ nvfp4_status moe_route(int32_t logits_type, const void* logits, int64_t ld, int6
   if (num_groups <= 0 || num_groups > num_experts || num_experts % num_groups != 0) return NVFP4_ERR_ARG;
   if (top_groups <= 0 || top_groups > num_groups) return NVFP4_ERR_ARG;
   if (top_k <= 0 || top_k > kMaxTopK || top_k > num_experts / num_groups * top_groups) return NVFP4_ERR_ARG;
-  if (T <= 0 || T * top_k > kMaxRows || ld < num_experts || ld > kMaxDim) return NVFP4_ERR_SHAPE;
+  if (T <= 0 || T > kMaxRows || T * top_k > kMaxRows || ld < num_experts || ld > kMaxDim) return NVFP4_ERR_SHAPE;
   if (!logits || !topk_ids || !topk_w) return NVFP4_ERR_NULL;
   if (!aligned(logits, (uintptr_t)type_bytes(logits_type)) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
       !aligned(bias, 4))

@@ -325,18 +325,17 @@ void f8_tiled(F8Args a, int gm, int vec) {
 #pragma unroll
   for (int i = 0; i < GROUPS; i++) sc[1][i] = 0.f;
 
-  // (a group's weight first: its activations' rows are still being looked up)
-#pragma unroll
-  for (int s = 0; s < S::D - 1; s++)
-#pragma unroll
-    for (int i = S::NX; i < S::NX + S::NW; i++) issue(s, s, i);
+  // stage by stage, as the waits count them; in a stage the weight first, because a group's
+  // activation rows are still being looked up
 #pragma unroll
   for (int s = 0; s < S::D - 1; s++) {
+#pragma unroll
+    for (int i = S::NX; i < S::NX + S::NW; i++) issue(s, s, i);
 #pragma unroll
     for (int i = 0; i < S::NX; i++) issue(s, s, i);
     if (S::NS) issue(s, s, S::NX + S::NW);
   }
-  wait_loads_barrier<(S::D - 2) * (S::NX + S::NS)>();
+  wait_loads_barrier<(S::D - 2) * S::LOADS>();
   read_w(0);
   read_x(0, 0, 0);
   wait_scales();

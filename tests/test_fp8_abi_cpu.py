@@ -121,7 +121,7 @@ def test_grouped_workspace_query(lib):
     (dict(t=2), ERR_ARG), (dict(E=0), ERR_ARG), (dict(E=4097, ld=5000), ERR_ARG), (dict(scoring=2), ERR_ARG), (dict(scoring=-1), ERR_ARG),
     (dict(gs=2), ERR_ARG), (dict(renorm=2), ERR_ARG), (dict(G=0), ERR_ARG), (dict(G=3, tg=1), ERR_ARG), (dict(G=256), ERR_ARG),
     (dict(tg=0), ERR_ARG), (dict(tg=2), ERR_ARG), (dict(k=0), ERR_ARG), (dict(k=-1), ERR_ARG), (dict(k=65), ERR_ARG), (dict(E=4, k=5), ERR_ARG),
-    (dict(G=16, tg=1, k=9), ERR_ARG), (dict(T=0), ERR_SHAPE), (dict(T=-4), ERR_SHAPE), (dict(T=1 << 20), ERR_SHAPE), (dict(ld=127), ERR_SHAPE),
+    (dict(G=16, tg=1, k=9), ERR_ARG), (dict(T=0), ERR_SHAPE), (dict(T=-4), ERR_SHAPE), (dict(T=1 << 61), ERR_SHAPE), (dict(T=1 << 62, k=4), ERR_SHAPE), (dict(T=1 << 20), ERR_SHAPE), (dict(ld=127), ERR_SHAPE),
     (dict(ld=1 << 31), ERR_SHAPE), (dict(l=None), ERR_NULL), (dict(ids=None), ERR_NULL), (dict(w=None), ERR_NULL), (dict(l=P + 2), ERR_ALIGN),
     (dict(t=0, l=P + 1), ERR_ALIGN), (dict(ids=P + 2), ERR_ALIGN), (dict(w=P + 2), ERR_ALIGN), (dict(bias=P + 2), ERR_ALIGN),
 ])

@@ -261,6 +261,24 @@ def test_linear_tiles(dev, M, N, K, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("M,N,K", [(700, 2100, 8336), (400, 3400, 16400)])
+def test_linear_tiles_long_rows(dev, M, N, K, kind):
+    """More blocks along K than a wave has lanes."""
+    say("linear tiles, long rows", kind, M, N, K)
+    rng = rng_of(16, M, N, K)
+    x, (c, s) = acts(rng, M, K), weight(rng, N, K)
+    (xd, xs), xv = act_operand(x, kind, dev)
+    w = ref.dequantize(c, s, 128)
+    keep = np.arange(0, M, 61)
+    want, mag = ref.linear(xv[keep], w)
+    at = torch.from_numpy(keep).to(dev)
+    y = nv.fp8_linear(xd, up(c, dev), up(s, dev), x_scales=xs)
+    assert_near(y[at], want, ref.tolerance(want, mag, K), (kind, M, N, K))
+    yb = nv.fp8_linear(xd, up(c, dev), up(s, dev), x_scales=xs, out_dtype=torch.bfloat16)
+    check_bf16(yb if kind == "bf16" else yb[at], y, want, ref.tolerance(want, mag, K), kind, xv[keep], w)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
 def test_linear_offsets_past_32_bits(dev, kind):
     """A weight, and activations, of more than 2^31 bytes: 512 and 509 rows over and over."""
     K, P, W = 8192, 509, 512
@@ -470,7 +488,7 @@ def lost_of(kind, xv, w, ids, per_route=False):
 GROUPED = [(1, 4, 1, 64, 32), (1, 128, 8, 256, 2048), (16, 128, 8, 256, 272), (5, 3, 3, 130, 112), (40, 6, 2, 64, 1056),
            (333, 24, 3, 66, 160), (200, 2, 1, 256, 512), (64, 300, 4, 256, 64), (700, 8, 2, 320, 288), (1500, 5, 2, 130, 128),
            (100, 128, 4, 128, 160), (300, 64, 2, 66, 528), (256, 40, 1, 512, 64), (257, 40, 1, 64, 80), (90, 200, 64, 64, 32), (4, 70, 64, 256, 64),
-           (900, 6, 3, 768, 400)]
+           (900, 6, 3, 768, 400), (260, 2, 2, 256, 8336)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
