@@ -11,12 +11,16 @@
 // (c, g) = c + 16g takes pieces g and 4 + g of its row's eight, k = 16g and 64 + 16g on.
 //  - FP8 activations, results in BF16: one MFMA over the step from zero, whose result is added
 //    times both scales. (It is less exact than fp32: see mfma_f8.)
-//  - otherwise the lane decodes its 32 codes to BF16 (for results in fp32 those of FP8 activations
-//    too), four MFMAs over 32 k each from zero, whose result is added times the scales.
+//  - otherwise the lane decodes its 32 codes to BF16 (for results in fp32 and SwiGLU those of FP8
+//    activations too), four MFMAs over 32 k each from zero, whose result is added times the scales.
 // The 16 weight rows of an MFMA lie in one block of 128, so its scale is the same for a wave: those
 // of 64 steps are loaded at once.
 // Loads past the rows, past K and past a wave's run are out of range: every step issues the
 // same number, which is what the counted waits go by.
+// Measured, weights from HBM: 16 x 12288 x 4096 BF16 11.0 us (50.5 MB, 4.6 TB/s; a copy of 2 GiB
+// reaches 4.9); one row of 4096 x 4096 4.0 us, which is the latency of a launch, one ring and the
+// sum over the waves; 32 experts of 4096 x 2048 for 16 tokens (top 4) 50 us with BF16 activations
+// (4.7 TB/s).
 #include "f8_device.hpp"
 #include "f8_kernels.hpp"
 #include "mx_routes.hpp"
@@ -24,19 +28,21 @@
 namespace nvfp4 {
 namespace {
 
-// XR activation rows (4, or TM tiles of 16), NT tiles of 16 weight rows, W waves, U steps in
+// XR activation rows (4 or 8, or TM tiles of 16), NT tiles of 16 weight rows, W waves, U steps in
 // the ring
 template <int ACT_, int XR_, int NT_, int W_, int U_>
 struct Cfg {
   static constexpr int ACT = ACT_, XR = XR_, TM = (XR_ + 15) / 16, NT = NT_, W = W_, U = U_;
   static constexpr bool F8 = ACT_ != FP8_ACT_BF16, FAST = ACT_ == FP8_ACT_FP8;
-  static constexpr int XMAX = F8 ? 2 * TM : XR / 4;  // 1 KiB loads of activations a step
-  static constexpr int SX = F8 ? 1 : 0;              // loads of their scales
+  static constexpr int XROWS = F8 ? 8 : 4, XMAX = XR / XROWS;  // 1 KiB loads of activations a step
+  static constexpr int SX = F8 ? 1 : 0;  // loads of their scales
   static constexpr int LOADS = 2 * NT + XMAX + SX;
-  static constexpr int W0 = 0, X0 = 2048 * NT, S0 = X0 + 1024 * XMAX, STEP = S0 + 256 * SX;
-  static constexpr int WS0 = STEP * U, RING = WS0 + 256 * NT;  // of a wave: steps, scales of the weight
+  static constexpr int W0 = 0, X0 = 2048 * NT, STEP = X0 + 1024 * XMAX;
+  // of a wave: steps, scales of the weight, two windows of activation scales (16 bytes a row)
+  static constexpr int WS0 = STEP * U, XS0 = WS0 + 256 * NT, RING = XS0 + 2048 * SX;
+  static_assert(U - 1 <= 4, "a window is in use until it is overwritten");
   static constexpr int PART = 1024 * NT * TM;  // partial sums of a wave
-  static constexpr int LDS = W * (RING > PART ? RING : PART);
+  static constexpr int WAVES = W * (RING > PART ? RING : PART), LDS = WAVES + 1024 * SX;  // (the sink)
   static_assert(NT <= 4 && TM <= 4 && LDS <= 160 * 1024, "");
 };
 
@@ -49,12 +55,12 @@ struct Operands {
 };
 
 // One wave's run [s0, s1) of steps over the rows whose lanes' offsets are wo, xo, xso; wso: where
-// its weight tiles' scales begin.
+// its weight tiles' scales begin; sink: 1 KiB of LDS that nobody reads.
 template <class C>
 __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, const uint8_t* ring_p,
                                           int s0, int s1, int K, const uint32_t* wo,
                                           const uint32_t* xo, uint32_t xso,
-                                          const uint32_t (&wso)[C::NT],
+                                          const uint32_t (&wso)[C::NT], uint32_t sink,
                                           f32x4 (&acc)[C::NT][C::TM]) {
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const auto issue = [&](int s, int u) {
@@ -78,7 +84,14 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
       }
       lds_load<16>(d.x, off, base + C::X0 + 1024 * i);
     }
-    if (C::F8) lds_load<4>(d.xs, in ? xso + 4 * s : kOutOfRange, base + C::S0);
+    if (C::F8) {
+      // scales of four steps at a time: a load costs by the cache lines that it looks up (against
+      // a load of 4 bytes a row and step: M 64 x 4096 x 4096 8.7 -> 8.2 us, 16 x 4096 x 14336
+      // 15.0 -> 13.9 us). Past the last row they are out of range, dword by dword.
+      const int n = s - s0;
+      lds_load<16>(d.xs, in && n % 4 == 0 ? xso + 4 * s : kOutOfRange,
+                   n % 4 == 0 ? ring + C::XS0 + n / 4 % 2 * 1024 : sink);
+    }
   };
   // the weight tiles' scales of 64 steps from s on
   const auto load_scales = [&](int s) {
@@ -106,12 +119,15 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
     float xs[C::TM];
 #pragma unroll
     for (int x = 0; x < C::TM; x++)
-      xs[x] = C::F8 ? *reinterpret_cast<const float*>(b + C::S0 + 4 * (16 * x + c)) : 1.f;
+      xs[x] = C::F8 ? reinterpret_cast<const float*>(ring_p + C::XS0 + (s - s0) / 4 % 2 * 1024 +
+                                                     16 * (16 * x + c))[(s - s0) % 4]
+                    : 1.f;
     // this lane's 32 k of activation row 16x + c: two pieces of codes, or four of BF16
     u32x4 xf[C::TM][C::FAST ? 2 : 4];
 #pragma unroll
     for (int x = 0; x < C::TM; x++) {
-      const int r = 16 * x + c;
+      // rows past the loaded ones read others' values, into columns that nobody stores
+      const int r = (16 * x + c) % (C::XROWS * C::XMAX);
       if constexpr (C::F8) {
         const u32x4 x0 = piece(b + C::X0, r, g), x1 = piece(b + C::X0, r, 4 + g);
         if constexpr (C::FAST) {
@@ -121,11 +137,9 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
           f8_decode32(x0, x1, xf[x]);
         }
       } else {
-        // rows past the loaded ones read others' values, into columns that nobody stores
-        const int rr = r % (4 * C::XMAX);
 #pragma unroll
         for (int j = 0; j < 4; j++)
-          xf[x][j] = *reinterpret_cast<const u32x4*>(b + C::X0 + 256 * rr + (((g + 4 * j) ^ (rr & 15)) << 4));
+          xf[x][j] = *reinterpret_cast<const u32x4*>(b + C::X0 + 256 * r + (((g + 4 * j) ^ (r & 15)) << 4));
       }
     }
 #pragma unroll
@@ -235,7 +249,7 @@ __global__ __launch_bounds__(64 * C::W) void f8_stream(F8Args a) {
   // this wave's run of steps
   const int per = (kb + C::W - 1) / C::W;
   const int s0 = wave * per, s1 = s0 + per < kb ? s0 + per : kb;
-  constexpr int WAVE = C::LDS / C::W;
+  constexpr int WAVE = C::WAVES / C::W;
   const uint8_t* ring_p = smem + wave * WAVE;
   const uint32_t ring = lds_address(smem) + wave * WAVE;
 
@@ -270,7 +284,7 @@ __global__ __launch_bounds__(64 * C::W) void f8_stream(F8Args a) {
       xo[i] = row >= 0 ? (uint32_t)row * xpitch + 16 * q : kOutOfRange;
     }
     if (C::F8) {
-      const int row = lane < 16 * C::TM ? x_row(lane) : -1;
+      const int row = lane < C::XR ? x_row(lane) : -1;
       xso = row >= 0 ? 4u * (uint32_t)row * (uint32_t)kb : kOutOfRange;
     }
     f32x4 acc[C::NT][C::TM];
@@ -278,7 +292,9 @@ __global__ __launch_bounds__(64 * C::W) void f8_stream(F8Args a) {
     for (int t = 0; t < C::NT; t++)
 #pragma unroll
       for (int x = 0; x < C::TM; x++) acc[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (s0 < s1) run_steps<C>(d, ring, ring_p, s0, s1, K, wo, xo, xso, wso, acc);
+    if (s0 < s1)
+      run_steps<C>(d, ring, ring_p, s0, s1, K, wo, xo, xso, wso,
+                   lds_address(smem) + C::W * WAVE, acc);
     // partial sums of this wave [NT][TM][64], in the bytes of its ring
     const auto part = [&](int w) { return reinterpret_cast<f32x4*>(smem + w * WAVE); };
 #pragma unroll
@@ -369,15 +385,15 @@ hipError_t launch_dense(const F8Args& a, hipStream_t stream) {
 template <int ACT>
 hipError_t launch_act(const F8Args& a, int64_t rows, hipStream_t stream) {
   constexpr bool F8 = ACT != FP8_ACT_BF16;
-  // a BF16 form of four rows loads no activations for the 12 others of the MFMA
+  // forms of eight rows (BF16: four) load no activations for the other ones of the MFMA
   if (a.ids || a.slots) {
-    constexpr int FEW = F8 ? 16 : 4;
+    constexpr int FEW = F8 ? 8 : 4;
     if constexpr (ACT != FP8_ACT_FP8) {
       if (a.swiglu) return rows <= 2 ? launch_rows<ACT, FEW, 4, 4, 2, true>(a, stream) : launch_rows<ACT, 16, 4, 4, 2, true>(a, stream);
     }
     return rows <= 2 ? launch_rows<ACT, FEW, 2, 2, 2, true>(a, stream) : launch_rows<ACT, 16, 2, 2, 2, true>(a, stream);
   }
-  if (rows <= 4) return launch_dense<ACT, F8 ? 16 : 4, F8 ? 3 : 2>(a, stream);
+  if (rows <= (F8 ? 8 : 4)) return launch_dense<ACT, F8 ? 8 : 4, F8 ? 3 : 2>(a, stream);
   if (rows <= 16) return launch_dense<ACT, 16, F8 ? 3 : 2>(a, stream);
   if (rows <= 32) return launch_rows<ACT, 32, 2, 4, 2>(a, stream);
   return launch_rows<ACT, F8 ? 64 : 48, 2, 4, 2>(a, stream);
