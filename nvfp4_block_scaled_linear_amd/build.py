@@ -22,7 +22,7 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 # into VALU FMAs (the per-block scale); in the accumulation-register form each of those
 # reads costs one v_accvgpr_read, so their MFMAs write ordinary VGPRs. The MXFP4 kernels'
 # scaled MFMAs in the accumulation-register form get their accumulators copied around in
-# every step.
+# every step; so it is with the FP8 ones, whose results the FMAs of the scales read at once.
 _VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 EXTRA = {f: _VGPR_FORM for f in ("stream.hip", "mx_stream.hip", "mx_tiled.hip", "f8_stream.hip", "f8_tiled.hip")}
 

@@ -75,7 +75,7 @@ bool fits(int64_t rows, int64_t pitch_bytes) { return rows * pitch_bytes < (int6
 // result is rounded to BF16 and nothing more: not fp32 ones, and not SwiGLU's, which are quantized
 // again. (What those sums lose moves block scales and codes: a prompt's layer, 2048 / 768, was
 // 0.0025 off its 64-bit result in the 2-norm, with fp32 sums 0.0017, most of it y's own rounding; its
-// gate_up takes 300 us against 210.)
+// gate_up takes 290 us against 200.)
 int kernel_kind(int32_t act_kind, bool plain_bf16) {
   return act_kind == FP8_ACT_FP8 && !plain_bf16 ? kF8Exact : act_kind;
 }
@@ -96,10 +96,10 @@ bool streams(int32_t kind, int64_t M, int64_t N) {
 }
 
 // Routes per active expert from which the grouped call works in tiles, and in tiles of 128
-// routes (see RoutePlan). 32 experts, top-4, 2048 / 1024: gate_up and down of 64 tokens take 35 + 23
-// us by slots and 30 + 25 in tiles (W8A8 37 + 20 and 29 + 23), of 96 tokens 42 + 28 and 30 + 26 (43 +
-// 25 and 30 + 24). 512 tokens take 44 + 37 in tiles of 64 and 59 + 45 in tiles of 128 (44 + 36 and 52
-// + 40), 1024 tokens 65 + 52 and 66 + 53 (62 + 51 and 56 + 46).
+// routes (see RoutePlan). 32 experts, top-4, 2048 / 1024: gate_up and down of 64 tokens take 36 + 22
+// us by slots and 30 + 24 in tiles (W8A8 39 + 20 and 31 + 23), of 96 tokens 42 + 28 and 30 + 25 (44 +
+// 25 and 31 + 23). 512 tokens take 44 + 36 in tiles of 64 and 58 + 45 in tiles of 128 (53 + 36 and 75
+// + 40), 1024 tokens 65 + 51 and 65 + 52 (79 + 50 and 77 + 47).
 constexpr int64_t kTiledRoutes = 8;
 constexpr int64_t kTile128Routes = 96;
 

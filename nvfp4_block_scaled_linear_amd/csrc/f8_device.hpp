@@ -16,8 +16,9 @@ constexpr float kF8Top = 448.0f;  // E4M3's largest value
 // drops what lies below 2^-13 of the largest one's power of two (measured; the sums of eights
 // are added as in fp32; the older 16x16x32 form does the same), at most 7 * 2^-13 of that
 // product, and about 3e-5 of a result by the 2-norm with unit normal activations, loud channels
-// among them. BF16 results are rounded by 2^-9 of themselves, and E4M3 activations by 2^-4. Where
-// fp32 is asked for, codes are decoded to BF16, whose MFMA sums in fp32, at half the rate.
+// among them. BF16 results are rounded by 2^-9 of themselves, and E4M3 activations by 2^-4. For
+// results in fp32, and for SwiGLU's, codes are decoded to BF16, whose MFMA sums in fp32, at half
+// the rate.
 __device__ __forceinline__ f32x4 mfma_f8(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x4 c) {
   const i32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
   const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};

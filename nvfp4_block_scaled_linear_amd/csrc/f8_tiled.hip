@@ -21,6 +21,11 @@
 //    weight rows of a group (SwiGLU: of gate, of up) lie in one block of scales, so their scale
 //    is a scalar: lane l of a wave holds that of the stage that is l on. The scales of activation
 //    rows come in windows of 16 bytes, four blocks at a time, through LDS.
+// Measured: 2048 x 14336 x 4096 W8A8 130 us (1.85 PFLOP/s), 8192 rows 450 us (2.14; the library's
+// product with one scale for all 403). There the matrix cores are busy 52 % of the cycles and the
+// vector units, with the scales' FMAs, 42 %, at 1.9 GHz: data of zeros, which take less power, run
+// 373 us; without the FMAs it would be 378, with loads from one hot line 405. BF16 activations 217
+// us, fp32 results of W8A8 238: both decode in the vector units.
 #include <type_traits>
 
 #include "f8_device.hpp"

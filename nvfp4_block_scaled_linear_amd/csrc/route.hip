@@ -1,15 +1,18 @@
 // Routing to experts (moe_route in fp8.h).
 //
-// One wave per token (many tokens: moe_route_many, below). Lane l holds the experts l * V + [0, V): the keys that they are picked by, as
-// 32-bit integers in the order of the floats that they stand for. The picks are top_k rounds of a
-// largest key over the wave (lane exchanges inside the vector unit, no LDS), ties to the lower
-// lane and index; lane j keeps pick j, and computes its weight in 64 bits at the end.
+// One wave per token (many tokens: moe_route_many, below). Lane l holds the experts l * V + [0, V):
+// the keys that they are picked by, as 32-bit integers in the order of the floats that they stand
+// for. The picks are top_k rounds of a largest key over the wave (lane exchanges inside the vector
+// unit, no LDS), ties to the lower lane and index; lane j keeps pick j, and computes its weight in
+// 64 bits at the end.
+// Measured: one token of 128 experts 2.9 us, 16 4.8, which is latency; 16384 of 256, groups and a
+// bias, 20 us (17 MB: 3.6 us to read), bound by the instructions of the rounds.
 //  - Without a bias the keys are the logits themselves: scores grow with them, so the order is
 //    exact.
 //  - Otherwise the keys are fp32 scores, good to near_of / 2. Where two picks in a row, the last pick
 //    and the next best, or a kept group and one that is not lie closer than that allows to tell
-//    apart (picks that are equal in logit and bias aside), the token is decided again by scores in 64 bits
-//    (decide64), a few tokens in a thousand where logits are spread like a router's.
+//    apart (picks that are equal in logit and bias aside), the token is decided again by scores in
+//    64 bits (decide64), a few tokens in a thousand where logits are spread like a router's.
 // Groups are scored by lane exchanges where a group is a power of two of lanes, up to 16, and by a
 // lane each, from keys in LDS, otherwise (scores: in decide64).
 #include "f8_kernels.hpp"
@@ -613,7 +616,9 @@ __global__ __launch_bounds__(256) void moe_route_many(RouteArgs a, int lds_bytes
   }
 }
 
-// From this many tokens on four go to a wave (a wave on each SIMD then).
+// From this many tokens on four go to a wave (a wave on each SIMD then). 256 experts, groups and a
+// bias, a wave per token against four to a wave: 1024 tokens 9.9 and 11.3 us, 4096 12.6 and 12.7,
+// 16384 25.6 and 19.4; 128 experts by softmax, 16384 tokens, 11.6 and 6.2.
 constexpr int64_t kManyTokens = 4096;
 
 template <int V, bool SCORES>
