@@ -39,10 +39,11 @@ struct Cfg {
   static constexpr int LOADS = 2 * NT + XMAX + SX;
   static constexpr int W0 = 0, X0 = 2048 * NT, STEP = X0 + 1024 * XMAX;
   // of a wave: steps, scales of the weight, two windows of activation scales (16 bytes a row)
-  static constexpr int WS0 = STEP * U, XS0 = WS0 + 256 * NT, RING = XS0 + 2048 * SX;
+  static constexpr int WIN = 16 * XR * SX;
+  static constexpr int WS0 = STEP * U, XS0 = WS0 + 256 * NT, RING = XS0 + 2 * WIN;
   static_assert(U - 1 <= 4, "a window is in use until it is overwritten");
   static constexpr int PART = 1024 * NT * TM;  // partial sums of a wave
-  static constexpr int WAVES = W * (RING > PART ? RING : PART), LDS = WAVES + 1024 * SX;  // (the sink)
+  static constexpr int WAVES = W * (RING > PART ? RING : PART), LDS = WAVES + WIN;  // (the sink)
   static_assert(NT <= 4 && TM <= 4 && LDS <= 160 * 1024, "");
 };
 
@@ -55,7 +56,7 @@ struct Operands {
 };
 
 // One wave's run [s0, s1) of steps over the rows whose lanes' offsets are wo, xo, xso; wso: where
-// its weight tiles' scales begin; sink: 1 KiB of LDS that nobody reads.
+// its weight tiles' scales begin; sink: C::WIN bytes of LDS that nobody reads.
 template <class C>
 __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, const uint8_t* ring_p,
                                           int s0, int s1, int K, const uint32_t* wo,
@@ -89,8 +90,9 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
       // a load of 4 bytes a row and step: M 64 x 4096 x 4096 8.7 -> 8.2 us, 16 x 4096 x 14336
       // 15.0 -> 13.9 us). Past the last row they are out of range, dword by dword.
       const int n = s - s0;
-      lds_load<16>(d.xs, in && n % 4 == 0 ? xso + 4 * s : kOutOfRange,
-                   n % 4 == 0 ? ring + C::XS0 + n / 4 % 2 * 1024 : sink);
+      if (lane < C::XR)
+        lds_load<16>(d.xs, in && n % 4 == 0 ? xso + 4 * s : kOutOfRange,
+                     n % 4 == 0 ? ring + C::XS0 + n / 4 % 2 * C::WIN : sink);
     }
   };
   // the weight tiles' scales of 64 steps from s on
@@ -119,8 +121,8 @@ __device__ __forceinline__ void run_steps(const Operands& d, uint32_t ring, cons
     float xs[C::TM];
 #pragma unroll
     for (int x = 0; x < C::TM; x++)
-      xs[x] = C::F8 ? reinterpret_cast<const float*>(ring_p + C::XS0 + (s - s0) / 4 % 2 * 1024 +
-                                                     16 * (16 * x + c))[(s - s0) % 4]
+      xs[x] = C::F8 ? reinterpret_cast<const float*>(ring_p + C::XS0 + (s - s0) / 4 % 2 * C::WIN +
+                                                     16 * ((16 * x + c) % C::XR))[(s - s0) % 4]
                     : 1.f;
     // this lane's 32 k of activation row 16x + c: two pieces of codes, or four of BF16
     u32x4 xf[C::TM][C::FAST ? 2 : 4];
