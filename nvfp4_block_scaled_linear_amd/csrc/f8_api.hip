@@ -96,11 +96,13 @@ bool streams(int32_t kind, int64_t M, int64_t N) {
 }
 
 // Routes per active expert from which the grouped call works in tiles, and in tiles of 128
-// routes (see RoutePlan). 32 experts, top-4, 2048 / 1024: gate_up and down of 64 tokens take 36 + 22
-// us by slots and 30 + 24 in tiles (W8A8 39 + 20 and 31 + 23), of 96 tokens 42 + 28 and 30 + 25 (44 +
-// 25 and 31 + 23). 512 tokens take 44 + 36 in tiles of 64 and 58 + 45 in tiles of 128 (53 + 36 and 75
-// + 40), 1024 tokens 65 + 51 and 65 + 52 (79 + 50 and 77 + 47).
-constexpr int64_t kTiledRoutes = 8;
+// routes (see RoutePlan); both calls of a layer have to agree, whatever their activations are.
+// gate_up and down of 128 experts, top-8, 2048 / 768: 64 tokens take 98 + 53 us by slots and 79 + 57
+// in tiles (W8A8 83 + 52 and 90 + 58), 96 tokens 101 + 56 and 80 + 57 (89 + 56 and 91 + 59); of 32
+// experts, top-4, 2048 / 1024: 48 tokens 31 + 21 and 29 + 24 (32 + 21 and 31 + 23), 96 tokens 42 + 28
+// and 30 + 25 (44 + 25 and 31 + 23). 512 tokens of the latter take 44 + 36 in tiles of 64 and 58 + 45
+// in tiles of 128 (53 + 36 and 75 + 40), 1024 tokens 65 + 51 and 65 + 52 (79 + 50 and 77 + 47).
+constexpr int64_t kTiledRoutes = 6;
 constexpr int64_t kTile128Routes = 96;
 
 }  // namespace

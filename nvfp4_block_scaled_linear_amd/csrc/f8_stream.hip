@@ -17,10 +17,10 @@
 // of 64 steps are loaded at once.
 // Loads past the rows, past K and past a wave's run are out of range: every step issues the
 // same number, which is what the counted waits go by.
-// Measured, weights from HBM: 16 x 12288 x 4096 BF16 11.0 us (50.5 MB, 4.6 TB/s; a copy of 2 GiB
-// reaches 4.9); one row of 4096 x 4096 4.0 us, which is the latency of a launch, one ring and the
-// sum over the waves; 32 experts of 4096 x 2048 for 16 tokens (top 4) 50 us with BF16 activations
-// (4.7 TB/s).
+// Measured, weights from HBM: 16 x 12288 x 4096 11 to 12 us (50.5 MB, 4.2 to 4.6 TB/s; a copy of 2
+// GiB reaches 4.9); one row of 4096 x 4096 4.0 us, which is the latency of a launch, one ring and the
+// sum over the waves; gate_up of 16 tokens, top-8 of 128 experts of 1536 x 2048, 50 us with BF16
+// activations (82 experts, 259 MB, 5.1 TB/s) and 56 in W8A8, whose sums in fp32 decode both sides.
 #include "f8_device.hpp"
 #include "f8_kernels.hpp"
 #include "mx_routes.hpp"
@@ -387,15 +387,23 @@ hipError_t launch_dense(const F8Args& a, hipStream_t stream) {
 template <int ACT>
 hipError_t launch_act(const F8Args& a, int64_t rows, hipStream_t stream) {
   constexpr bool F8 = ACT != FP8_ACT_BF16;
-  // forms of eight rows (BF16: four) load no activations for the other ones of the MFMA
+  // Forms of eight rows (BF16: four) load no activations for the other ones of the MFMA. By expert,
+  // where two of their workgroups fit a CU and two of the larger ones do not, they also win with a
+  // second turn over the weight, from L2. 128 experts, top-8, 2048 / 768: W8A8 gate_up and down of 64
+  // tokens (four routes an expert) take 83 + 52 us eight rows at a time, 103 + 55 in sixteen; BF16
+  // gate_up of 48 tokens 79 us with four rows, 96 with sixteen (down 50 with eight, 57), of 96
+  // tokens 112 and 101 (56, 60), of 32 experts, top-4, 2048 / 1024, 32 tokens 34 and 29 (19 and 20).
+  constexpr int FEW = F8 ? 8 : 4;
   if (a.ids || a.slots) {
-    constexpr int FEW = F8 ? 8 : 4;
     if constexpr (ACT != FP8_ACT_FP8) {
-      if (a.swiglu) return rows <= 2 ? launch_rows<ACT, FEW, 4, 4, 2, true>(a, stream) : launch_rows<ACT, 16, 4, 4, 2, true>(a, stream);
+      if (a.swiglu)
+        return F8 || rows <= 3 ? launch_rows<ACT, FEW, 4, 4, 2, true>(a, stream)
+                               : launch_rows<ACT, F8 ? FEW : 16, 4, 4, 2, true>(a, stream);
     }
-    return rows <= 2 ? launch_rows<ACT, FEW, 2, 2, 2, true>(a, stream) : launch_rows<ACT, 16, 2, 2, 2, true>(a, stream);
+    return rows <= 2 ? launch_rows<ACT, FEW, 2, 2, 2, true>(a, stream)
+                     : launch_rows<ACT, 8, 2, 2, 2, true>(a, stream);
   }
-  if (rows <= (F8 ? 8 : 4)) return launch_dense<ACT, F8 ? 8 : 4, F8 ? 3 : 2>(a, stream);
+  if (rows <= FEW) return launch_dense<ACT, FEW, F8 ? 3 : 2>(a, stream);
   if (rows <= 16) return launch_dense<ACT, 16, F8 ? 3 : 2>(a, stream);
   if (rows <= 32) return launch_rows<ACT, 32, 2, 4, 2>(a, stream);
   return launch_rows<ACT, F8 ? 64 : 48, 2, 4, 2>(a, stream);
