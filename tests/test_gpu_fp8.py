@@ -520,6 +520,25 @@ def test_grouped_prompts(dev, T, E, k, N, K, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("popular", [False, True])
+@pytest.mark.parametrize("T,E,k,N,K", [(20, 40, 5, 256, 1296), (28, 40, 5, 130, 640), (42, 40, 5, 256, 784), (47, 40, 5, 64, 2064),
+                                       (110, 200, 5, 256, 1296), (160, 200, 5, 128, 656), (235, 200, 5, 256, 400), (240, 200, 5, 128, 400)])
+def test_grouped_a_few_routes_an_expert(dev, T, E, k, N, K, popular, kind):
+    """Two to six routes an expert, or one with many: more of them than a workgroup takes at once."""
+    say("grouped few routes", kind, T, E, k, N, K, popular)
+    rng = rng_of(26, T, E, k, N, K, popular)
+    ids, tw = routes(rng, T, E, k)
+    if popular:
+        at = np.flatnonzero((ids != 7).all(axis=1))[: T // 2]
+        ids[at, 1] = 7
+    x, (c, s) = acts(rng, T, K), weight(rng, E, N, K)
+    (xd, xs), xv = act_operand(x, kind, dev)
+    w = ref.dequantize(c, s, 128)
+    y, mag, _ = route_rows(xv, w, ids, False)
+    check_forms((xd, up(c, dev), up(s, dev), up(ids, dev)), xs, y, mag, tw, T, k, N, K, dev, lost_of(kind, xv, w, ids))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
 @pytest.mark.parametrize("T,E,k", [(9, 7, 3), (120, 40, 5), (300, 7, 3), (2500, 4, 2)])
 def test_grouped_bad_routes(dev, T, E, k, kind):
     """Ids out of range and repeated: flagged, their rows zero, the others as without them."""
