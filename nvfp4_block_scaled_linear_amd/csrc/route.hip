@@ -158,17 +158,22 @@ __device__ __forceinline__ void load_bias(const RouteArgs& a, int first, int ste
   for (int i = 0; i < V; i++) b[i] = a.bias[first + i * step < last ? first + i * step : last];
 }
 
-// The picks of token t by scores in 64 bits, by a whole wave: id of pick `lane`, or -1. Lane l has
-// experts l * V + [0, V); LDS (E + G doubles) serves groups that are no power of two of lanes.
-template <int V>
+// The picks of token t by a whole wave, by keys of 64 bits: scores, or without SCORES the logits
+// themselves, which scores of 64 bits do not tell apart everywhere (sigmoids above 37 are 1, so is
+// exp of 1e-20, and exp of -800 is 0). Returns the id of pick `lane`, or -1. Lane l has experts
+// l * V + [0, V); LDS (E + G doubles) serves groups that are no power of two of lanes.
+template <int V, bool SCORES>
 __device__ __forceinline__ int32_t decide64(const RouteArgs& a, int64_t t, double* lds) {
   const int lane = threadIdx.x & 63, E = a.num_experts, G = a.num_groups;
   const double none = (double)minus_inf();
   float l[V], bias[V];
-  load_bias<V>(a, lane * V, 1, bias);
+  if (SCORES) load_bias<V>(a, lane * V, 1, bias);
   load_logits<V>(a, t, lane * V, 1, l);
   double key[V];
-  if (a.scoring == ROUTE_SOFTMAX) {
+  if (!SCORES) {
+#pragma unroll
+    for (int i = 0; i < V; i++) key[i] = (double)l[i];
+  } else if (a.scoring == ROUTE_SOFTMAX) {
     int32_t m = ordered(l[0]);
 #pragma unroll
     for (int i = 1; i < V; i++) m = larger(m, ordered(l[i]));
@@ -186,8 +191,10 @@ __device__ __forceinline__ int32_t decide64(const RouteArgs& a, int64_t t, doubl
 #pragma unroll
     for (int i = 0; i < V; i++) key[i] = 1.0 / (1.0 + exp(-(double)l[i]));
   }
+  if (SCORES) {
 #pragma unroll
-  for (int i = 0; i < V; i++) key[i] = l[i] > minus_inf() && bias[i] > minus_inf() ? key[i] + (double)bias[i] : none;
+    for (int i = 0; i < V; i++) key[i] = l[i] > minus_inf() && bias[i] > minus_inf() ? key[i] + (double)bias[i] : none;
+  }
   if (G > 1) {
     double* const best = lds + E;
 #pragma unroll
@@ -396,7 +403,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int group_s
   }
   if (SCORES && near) {
     wave_lds_fence();
-    id = decide64<V>(a, t, reinterpret_cast<double*>(lds));
+    id = decide64<V, true>(a, t, reinterpret_cast<double*>(lds));
   }
   // weights: s of the picks, in 64 bits
   const float mine = id >= 0 ? logit_of(a, t, id) : minus_inf();
@@ -425,7 +432,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int group_s
 // The low bits of a key hold V - 1 - i in place of its own (sorting goes by minimum and maximum of
 // one register, and of equal keys the lower i, then the lower lane, is the lower expert). So keys are
 // good to 2^-19 of themselves (V = 16): exact for BF16 logits, otherwise `near` counts that in, and
-// fp32 logits that are closer are decided by decide64 too.
+// fp32 logits that are closer are decided by decide64 too, in their own order.
 template <int V, bool SCORES>
 __global__ __launch_bounds__(256) void moe_route_many(RouteArgs a, int lds_bytes) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -591,7 +598,7 @@ __global__ __launch_bounds__(256) void moe_route_many(RouteArgs a, int lds_bytes
   if (uint64_t undecided = __ballot(near && have && l16 == 0)) {
     for (; undecided; undecided &= undecided - 1) {
       const int r = __builtin_ctzll(undecided) >> 4;
-      const int32_t ids = decide64<V / 4>(a, t0 + r, reinterpret_cast<double*>(smem + wave * lds_bytes));
+      const int32_t ids = decide64<V / 4, SCORES>(a, t0 + r, reinterpret_cast<double*>(smem + wave * lds_bytes));
       const int32_t other = __shfl(ids, l16, 64);
       if (row == r) id = other;
       wave_lds_fence();

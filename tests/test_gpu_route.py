@@ -135,6 +135,44 @@ def test_many_tokens(dev, case, scoring, with_bias, group_score):
         check(l, k, dev, 0.5 * rng.integers(0, 2, E), torch.bfloat16, **kw)
 
 
+def extreme_logits(T, E, rng):
+    """fp32 rows, a quarter each: scores that round to 1 in 64 bits, scores that round to 0, logits that differ in
+    their last bits only, and logits near 0 whose scores are all alike; most have ties among the best."""
+    l = np.empty((T, E), np.float32)
+    a, b, c = T // 4, T // 2, 3 * T // 4
+    l[:a] = 0.5 * rng.integers(60, 161, (a, E))
+    l[a:b] = 50.0 * rng.integers(-40, 41, (b - a, E))
+    l[b:c] = np.float32(45) + np.spacing(np.float32(45)) * rng.integers(-40, 41, (c - b, E))
+    l[c:] = 1e-30 * rng.integers(-40, 41, (T - c, E))
+    return l
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top", [(60, 4, 1, 1), (64, 8, 2, 1), (96, 6, 3, 2), (128, 8, 1, 1), (128, 1, 8, 3), (256, 8, 8, 4), (256, 15, 1, 1)])
+def test_without_bias_the_order_is_that_of_the_logits(dev, E, k, groups, top, scoring):
+    """Also where scores in 64 bits are equal, for few tokens and for many."""
+    l = extreme_logits(4100, E, np.random.default_rng([15, E, k]))
+    kw = dict(scoring=scoring, groups=groups, top_groups=top)
+    ids, _ = check(l, k, dev, **kw)
+    few, _ = check(l[:4095], k, dev, **kw)
+    assert torch.equal(ids[:4095], few)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias,groups,top,group_score", [(False, 1, 1, "max"), (True, 1, 1, "max"), (False, 4, 2, "max"), (True, 4, 2, "max"),
+                                                               (False, 4, 2, "top2"), (True, 4, 2, "top2")])
+def test_a_tokens_experts_do_not_depend_on_the_others(dev, with_bias, groups, top, group_score, scoring):
+    rng = np.random.default_rng([16, groups])
+    E = 128
+    l = extreme_logits(4400, E, rng)
+    l[4100:] = 2 * rng.standard_normal((300, E))
+    l = torch.from_numpy(l[rng.permutation(len(l))]).to(dev)
+    bias = torch.from_numpy((0.25 * rng.integers(0, 3, E)).astype(np.float32)).to(dev) if with_bias else None
+    kw = dict(scoring=scoring, bias=bias, groups=groups, top_groups=top, group_score=group_score)
+    ids, _ = nv.moe_route(l, 8, **kw)
+    parts = [nv.moe_route(part, 8, **kw)[0] for part in l.split(1100)]
+    assert torch.equal(ids, torch.cat(parts))
+
 def test_close_scores(dev):
     """Scores with a bias that differ by less than fp32 can hold are told apart."""
     rng = np.random.default_rng(12)
