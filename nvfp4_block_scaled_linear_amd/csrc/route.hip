@@ -266,12 +266,14 @@ __device__ __forceinline__ void group_best2(int shift, int32_t& first, int32_t& 
   if (shift >= 4) merge(from_lane<kMirror16>(first), from_lane<kMirror16>(second));
 }
 
-// A group's score as a key, and how large (as a positive float's bits) what it is made of is.
+// A group's score as a key, and how large (as a positive float's bits) what it is made of is. Two low
+// biases may add up to less than fp32 holds: the group is open all the same and must not look like a
+// closed one (and infinitely large, it is close to every other).
 __device__ __forceinline__ int32_t group_score(const RouteArgs& a, int32_t first, int32_t second, int32_t* size) {
   const bool two = a.group_score == ROUTE_GROUP_TOP2 && second > kNone;
   const float f = unordered(first), s = two ? unordered(second) : 0.0f;
   *size = first > kNone ? __float_as_int(2.0f + fabsf(f) + fabsf(s)) : 0;
-  return ordered(f + s + 0.0f);
+  return first > kNone ? ordered(fmaxf(f + s, -kLargest) + 0.0f) : kNone;
 }
 
 // V experts a lane; SCORES: keys are scores. group_shift: lanes of a group as a power of two, or

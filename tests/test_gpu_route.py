@@ -173,6 +173,21 @@ def test_a_tokens_experts_do_not_depend_on_the_others(dev, with_bias, groups, to
     parts = [nv.moe_route(part, 8, **kw)[0] for part in l.split(1100)]
     assert torch.equal(ids, torch.cat(parts))
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [5, 4099])
+@pytest.mark.parametrize("E", [64, 128, 256])
+def test_groups_masked_by_low_biases(dev, E, T, scoring):
+    """Groups whose biases are the type's lowest value, or low enough for the sum of two to pass it, come
+    before closed ones and in the order of their sums in 64 bits."""
+    rng = np.random.default_rng([17, E, T])
+    l = rng.standard_normal((T, E))
+    least = float(np.finfo(np.float32).min)
+    group = np.arange(E) // (E // 4)
+    for low in ([-np.inf, least, -2e38, -3e38], [least, -np.inf, -2.5e38, -np.inf], [-np.inf, least, -np.inf, 0.1], [least, -2e38, least, -2e38]):
+        for top in (1, 2, 3):
+            check(l, 15, dev, np.array(low)[group], scoring=scoring, groups=4, top_groups=top, group_score="top2")
+
+
 def test_close_scores(dev):
     """Scores with a bias that differ by less than fp32 can hold are told apart."""
     rng = np.random.default_rng(12)
