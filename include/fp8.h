@@ -143,8 +143,10 @@ enum { ROUTE_GROUP_MAX = 0, ROUTE_GROUP_TOP2 = 1 };
  *   topk_ids[t] holds the top_k best experts by descending c, topk_w[t] their s (without the bias):
  *   divided by the sum of the picked ones' with renormalize (zeros if that is 0), then times
  *   `scale`.
- *   Of equals, experts or groups, the lower index comes first. Scores are compared as real
- *   numbers are, to 64-bit precision: without bias, in the logits' own order.
+ *   Of equals, experts or groups, the lower index comes first. Without a bias, and unless groups
+ *   are scored by their two best, experts and groups are compared by the logits themselves, whose
+ *   order is that of the scores. Otherwise they are compared by c in 64 bits, where scores that
+ *   round to the same number are equals (sigmoids of logits above 37; softmax's that are 0).
  *   Where fewer than top_k experts are open to a token (a masked row), the rest of its ids are -1
  *   and their weights 0, which the grouped calls take as dropped routes.
  * 1 <= top_k <= 64, num_experts <= 4096, top_k at most the experts of top_groups groups.

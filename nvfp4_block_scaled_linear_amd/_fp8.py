@@ -224,8 +224,9 @@ def moe_route(logits, top_k, *, scoring="softmax", bias=None, groups=1, top_grou
     every format take them. Scores are a softmax over the experts or sigmoids; `bias` [E] fp32 is
     added to choose by, not to the weights. With groups > 1 only the top_groups (all when None)
     best of as many equal groups of experts are chosen from, a group's score being its best
-    expert's ("max") or the sum of its two best ("top2"). renormalize divides the weights by
-    their sum; `scale` multiplies them. Experts whose logit is -inf or NaN are not chosen: where
+    expert's ("max") or the sum of its two best ("top2"). With a bias, or groups by "top2", scores
+    are compared in 64 bits, otherwise the logits; of equals the lower index comes first.
+    renormalize divides the weights by their sum; `scale` multiplies them. Experts whose logit is -inf or NaN are not chosen: where
     they leave fewer than top_k, ids are -1 and weights 0, routes that grouped_linear drops."""
     index = _device(logits)
     T, E, ld = _rows(logits, "logits", _TYPES)

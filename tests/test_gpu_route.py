@@ -188,6 +188,24 @@ def test_groups_masked_by_low_biases(dev, E, T, scoring):
             check(l, 15, dev, np.array(low)[group], scoring=scoring, groups=4, top_groups=top, group_score="top2")
 
 
+@pytest.mark.parametrize("T", [3, 4099])
+def test_scores_that_round_to_the_same_number_are_equals(dev, T):
+    """Groups by their two best, or a bias, compare scores: sigmoids of 40 and of 60 are both 1 in 64 bits, and
+    softmax's of -800 and of -900 below 0 both 0. Without either the logits count."""
+    l = torch.full((T, 32), 40.0, device=dev)
+    l[:, 5] = 60.0
+    l[:, 20] = 50.0
+    kw = dict(scoring="sigmoid", groups=2)
+    for more in (dict(group_score="top2"), dict(bias=torch.zeros(32, device=dev)), dict(group_score="top2", bias=torch.zeros(32, device=dev))):
+        assert (nv.moe_route(l, 3, **kw, **more)[0].cpu() == torch.tensor([0, 1, 2])).all()
+    assert (nv.moe_route(l, 3, **kw)[0].cpu() == torch.tensor([5, 20, 0])).all()
+    l = torch.full((T, 32), -900.0, device=dev)
+    l[:, 7], l[:, 9] = 0.0, -800.0
+    for more in (dict(group_score="top2"), dict(bias=torch.zeros(32, device=dev))):
+        assert (nv.moe_route(l, 3, groups=2, **more)[0].cpu() == torch.tensor([7, 0, 1])).all()
+    assert (nv.moe_route(l, 3, groups=2)[0].cpu() == torch.tensor([7, 9, 0])).all()
+
+
 def test_close_scores(dev):
     """Scores with a bias that differ by less than fp32 can hold are told apart."""
     rng = np.random.default_rng(12)
