@@ -89,14 +89,19 @@ int64_t x_pitch(int32_t act_kind, int64_t ldx) { return act_kind == FP8_ACT_FP8 
 // take 9.0 against 18.7, 512 16.4 against 18.9, 768 25.4 against 19.5; with fp32 results 512 19.9
 // against 26.9, 768 28.8 against 27.6. Both sides grow with K, tiles less while launches of few
 // stages cost their latency: with K = 512 704 runs take 10.7 against 7.4 (BF16), with 1024 448 take
-// 9.0 against 7.7 (W8A8).
+// 9.0 against 7.7 (W8A8). (On the same operands again and again, which stay in the last-level
+// cache; with weights from HBM up to 3 us more.) The borders lie between those figures and know
+// nothing of K: two of the pairs above fall on their slower side, BF16's 768 runs, which go to tiles,
+// and W8A8's 448 with K = 1024, which stream.
 bool streams(int32_t kind, int64_t M, int64_t N) {
   const int64_t rows = kind == FP8_ACT_BF16 ? 48 : 64, most = kind == FP8_ACT_BF16 ? 600 : kind == FP8_ACT_FP8 ? 550 : 700;
   return M <= 32 || (M + rows - 1) / rows * ((N + 31) / 32) <= most;
 }
 
 // Routes per active expert from which the grouped call works in tiles, and in tiles of 128
-// routes (see RoutePlan); both calls of a layer have to agree, whatever their activations are.
+// routes (see RoutePlan); both calls of a layer have to agree, whatever their activations are, so
+// the borders are a middle between the kinds: BF16 layers of four routes an expert are 11 % slower
+// by slots, W8A8 ones of six 3 % slower in tiles.
 // gate_up and down of 128 experts, top-8, 2048 / 768: 64 tokens take 98 + 53 us by slots and 79 + 57
 // in tiles (W8A8 83 + 52 and 90 + 58), 96 tokens 101 + 56 and 80 + 57 (89 + 56 and 91 + 59); of 32
 // experts, top-4, 2048 / 1024: 48 tokens 31 + 21 and 29 + 24 (32 + 21 and 31 + 23), 96 tokens 42 + 28

@@ -1,7 +1,7 @@
 // FP8 quantizer and its way back (rules in fp8.h), and the scans of check mode. Bound by memory:
-// 2 or 4 bytes of a value on one side, 1 + 4/128 on the other. Measured, 2048 x 14336 BF16: 16 us
-// (89 MB, 5.5 TB/s, part of it the last-level cache's), the way back 17; 16 x 4096 3.1 and 2.4,
-// the latency of a launch.
+// 2 or 4 bytes of a value on one side, 1 + 4/128 on the other. Measured, 2048 x 14336 BF16: 16 to 18
+// us (89 MB, 5.1 TB/s), from fp32 28 (149 MB), the way back 17; a weight of 14336 x 4096 36 (176 MB,
+// 4.9 TB/s), from fp32 55 (294 MB); 16 x 4096 3.1 and 2.5, the latency of a launch.
 //
 // Eight lanes take a block of 128 k of a row, 16 values per lane, so that the block's largest
 // value is three exchanges inside the eight and a lane's codes are one 16-byte store. A weight's

@@ -19,8 +19,8 @@
 // same number, which is what the counted waits go by.
 // Measured, weights from HBM: 16 x 12288 x 4096 11 to 12 us (50.5 MB, 4.2 to 4.6 TB/s; a copy of 2
 // GiB reaches 4.9); one row of 4096 x 4096 4.0 us, which is the latency of a launch, one ring and the
-// sum over the waves; gate_up of 16 tokens, top-8 of 128 experts of 1536 x 2048, 50 us with BF16
-// activations (82 experts, 259 MB, 5.1 TB/s) and 56 in W8A8, whose sums in fp32 decode both sides.
+// sum over the waves; gate_up of 16 tokens, top-8 of 128 experts of 1536 x 2048, 51 us with BF16
+// activations (82 experts, 259 MB, 5.1 TB/s) and 53 in W8A8, whose sums in fp32 decode both sides.
 #include "f8_device.hpp"
 #include "f8_kernels.hpp"
 #include "mx_routes.hpp"

@@ -21,11 +21,11 @@
 //    weight rows of a group (SwiGLU: of gate, of up) lie in one block of scales, so their scale
 //    is a scalar: lane l of a wave holds that of the stage that is l on. The scales of activation
 //    rows come in windows of 16 bytes, four blocks at a time, through LDS.
-// Measured: 2048 x 14336 x 4096 W8A8 130 us (1.85 PFLOP/s), 8192 rows 450 us (2.14; the library's
-// product with one scale for all 403). There the matrix cores are busy 52 % of the cycles and the
-// vector units, with the scales' FMAs, 42 %, at 1.9 GHz: data of zeros, which take less power, run
-// 373 us; without the FMAs it would be 378, with loads from one hot line 405. BF16 activations 217
-// us, fp32 results of W8A8 238: both decode in the vector units.
+// Measured: 2048 x 14336 x 4096 W8A8 129 us (1.86 PFLOP/s), 8192 rows 447 us (2.15; the library's
+// product with one scale for all 403). There the matrix cores are busy 50 % of the cycles and the
+// vector units, with the scales' FMAs, 41 %, at 1.97 GHz: data of zeros, which take less power, run
+// 373 us; without the FMAs it would be 378, with loads from one hot line 405. BF16 activations 214
+// us, fp32 results of W8A8 242: both decode in the vector units.
 #include <type_traits>
 
 #include "f8_device.hpp"
@@ -518,7 +518,8 @@ hipError_t launch_shape(const F8Args& a, hipStream_t stream) {
 // in, times what a stage of 128 k costs in such a tile (in 10 ns, K = 4096, rounds that are full or
 // nearly so: W8A8 512 x 4096 in 256 tiles of 64 x 128 takes 19.8 us, 1024 x 4096 in 256 of 128 x 128
 // 25.6, 1024 x 8192 in 256 of 128 x 256 38.2, 4096 x 4096 in 256 of 256 x 256 61). Two of the smallest
-// fit a CU, and are done together sooner than one after the other (1024 tiles take 49 us). 1500 x
+// fit a CU, and are done together sooner than one after the other (1024 tiles take 49 us; 512, which
+// 1024 x 4096 goes to, 28, so the choice is 2 us off there). 1500 x
 // 6000 x 2048 takes 33 us in 144 tiles of 256 x 256, 39 in 288 of 128 x 256. The fp32 results of W8A8
 // decode both operands, which leaves no registers for the largest tile.
 struct TileCost {
