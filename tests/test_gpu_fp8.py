@@ -349,6 +349,25 @@ def test_linear_pitched_views_and_what_lies_around(dev, M, kind):
         assert (rest == 7).all()
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (9, 33)])
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_linear_every_pair_of_codes(dev, kind, rows, cols, out):
+    """Rows of one code each, subnormal ones among them: 144 equal products, whose sums of at most 128 are
+    exact in 32 bits, as are these times powers of two, and of which no instruction drops anything."""
+    K, n = 144, 254
+    codes = np.concatenate([np.arange(127), np.arange(128, 255)]).astype(np.uint8)
+    x, w = (np.tile(np.repeat(codes[:, None], K, 1), (many, 1)) for many in (rows, cols))
+    xs, ws = np.full((rows * n, 2), 2.0 ** -3, np.float32), np.full((ref.blocks(cols * n), 2), 4.0, np.float32)
+    want = torch.from_numpy(K * 0.5 * np.multiply.outer(ref.TABLE[codes], ref.TABLE[codes])).float().to(out).to(dev)
+    if kind == "bf16":
+        a, a_s = torch.from_numpy(ref.dequantize(x, xs)).to(torch.bfloat16).to(dev), None
+    else:
+        a, a_s = up(x, dev), up(xs, dev)
+    y = nv.fp8_linear(a, up(w, dev), up(ws, dev), x_scales=a_s, out_dtype=out)
+    assert torch.equal(y.view(rows, n, cols, n), want[None, :, None, :].expand(rows, n, cols, n))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 @pytest.mark.parametrize("M", [1, 20, 150, 400])
 def test_linear_scales_of_every_size(dev, M, kind):
